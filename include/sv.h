@@ -5,8 +5,11 @@
  * speculative decoding: the per-row verify length from the drafter's
  * survival confidences (sv_schedule, sv_schedule_admit), batched draft
  * verification by speculative rejection sampling (sv_verify), the same
- * verification with the vocabulary split across ranks (sv_vp_*), and the
- * confidence head's per-position temperature (sv_sts_*).
+ * verification with the vocabulary split across ranks (sv_vp_*), the
+ * confidence head's per-position temperature (sv_sts_*), and the two steps
+ * around a verification: the logits of the output head from 4-bit weights
+ * (sv_head_w4) under each request's rules (sv_logits_process), and the token
+ * history that the rules read and the emitted tokens feed (sv_history_*).
  *
  * Conventions for every entry point:
  *  - Pointers named as device pointers must be CUDA device memory (or
@@ -53,6 +56,13 @@ typedef enum { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
 #define SV_NOTE_ZERO_RESIDUAL   8   /* informational: a rejection left zero residual mass (drew from p_j) */
 #define SV_NOTE_CDF_FALLBACK   16   /* informational: rounding put the CDF target past the total */
 #define SV_NOTE_TIMEOUT        32   /* an internal wait exceeded its 1 s bound; outputs are undefined */
+
+/* Further bits, OR-ed in by sv_history_* and sv_logits_process. */
+#define SV_ROW_BAD_SLOT        64   /* a history slot outside [0, R) */
+#define SV_ROW_BAD_PENALTY    128   /* repetition not finite and > 0, or another penalty not finite */
+#define SV_ROW_BAD_BIAS       256   /* a bias of NaN or +inf, or a bias list outside its arrays */
+#define SV_ROW_BAD_MASK       512   /* a mask index outside [-1, n_masks) */
+#define SV_ROW_EMPTY_MASK    1024   /* a mask that allows no token: its logits are all -inf */
 
 /* Supported sizes. */
 #define SV_MAX_K  64
@@ -537,6 +547,176 @@ sv_status sv_verify_host(const void *target_logits, const void *draft_logits, sv
                          int64_t row_base, int32_t *out_tokens, int32_t *out_accept_len,
                          int32_t *lengths, int32_t *status, int levelwise, void *workspace,
                          size_t workspace_bytes, size_t *h2d_bytes, void *stream);
+
+/*
+ * Token history: sv_history_reset, sv_history_add.
+ *
+ * The tokens a request has seen, as the penalties of sv_logits_process need
+ * them.  The pages leave this state to the serving engine; it stands here
+ * because a verification step both reads it (the target's distribution at
+ * position i depends on the tokens before it) and advances it (by the
+ * accepted prefix and the token after it).
+ *
+ * A history holds R slots over a vocabulary of V tokens, W = ceil(V / 32):
+ * token v is bit v % 32 of word v / 32 of its slot's bit planes.  All three
+ * arrays are the caller's; zero-filled memory is an empty history.
+ */
+typedef struct {
+    uint32_t *prompt_bits;   /* device [R, W]: tokens of the prompt */
+    uint32_t *output_bits;   /* device [R, W]: tokens with output_counts > 0 */
+    int32_t *output_counts;  /* device [R, V]: how often each token was emitted */
+    int R, V;                /* R >= 1, 1 <= V <= SV_MAX_V */
+} sv_history;
+
+typedef enum { SV_HISTORY_PROMPT = 0, SV_HISTORY_OUTPUT = 1 } sv_history_kind;
+
+/*
+ * sv_history_reset -- empty the slots slots[0..n-1] (slots 0..n-1 if slots is
+ * NULL).  Only the counts whose output bit is set are written, so a slot's
+ * reset costs its bit planes, not its V counts.
+ *   slots   device int32 [n], nullable; a slot may be listed more than once; one
+ *           outside [0, R) is skipped (SV_ROW_BAD_SLOT).
+ *   n       >= 0; with slots NULL at most R.
+ *   status  device int32, nullable; bits OR-ed in.
+ * Returns SV_OK, SV_ERR_ARG, SV_ERR_SHAPE or SV_ERR_CUDA.
+ */
+sv_status sv_history_reset(const sv_history *history, const int32_t *slots, int n,
+                           int32_t *status, void *stream);
+
+/*
+ * sv_history_add -- append the first n_b = lens[b] + extra tokens of each row
+ * to its slot: kind SV_HISTORY_PROMPT sets prompt bits, SV_HISTORY_OUTPUT
+ * counts the tokens and sets output bits.  With tokens = out_tokens,
+ * lens = out_accept_len, S = K + 1 and extra = 1 it takes sv_verify's results
+ * as they are (an invalid row, -1, appends nothing).
+ *   slots   device int32 [B], nullable (row b is slot b, B <= R); two rows
+ *           may share a slot.
+ *   tokens  device int32 [B, S]; entries from n_b on are not read.  One
+ *           outside [0, V) is skipped (SV_ROW_BAD_TOKEN).
+ *   lens    device int32 [B], nullable (n_b = S).  A row with n_b outside
+ *           [0, S] appends nothing (SV_ROW_BAD_LENGTH).
+ *   B, S    B >= 0, S >= 0.
+ *   status  device int32, nullable; bits OR-ed in.
+ * Counts and bits are updated by integer atomics: the result does not depend
+ * on their order, and calls on several streams may share a history (a call
+ * that reads it has to be ordered after them).
+ * Returns SV_OK, SV_ERR_ARG, SV_ERR_SHAPE or SV_ERR_CUDA.
+ */
+sv_status sv_history_add(const sv_history *history, const int32_t *slots, int B,
+                         const int32_t *tokens, int S, const int32_t *lens, int extra,
+                         sv_history_kind kind, int32_t *status, void *stream);
+
+/*
+ * sv_logit_rules -- what a request asks of its logits.  Every part may be
+ * absent; arrays over rows are indexed by the batch row b.
+ */
+typedef struct {
+    const sv_history *history;   /* HOST, nullable (an empty history) */
+    const int32_t *slots;        /* device int32 [B], nullable: row b reads slot b */
+    const float *repetition;     /* device [B], nullable (1): finite, > 0 */
+    const float *frequency;      /* device [B], nullable (0): finite */
+    const float *presence;       /* device [B], nullable (0): finite */
+    const int32_t *bias_begin;   /* device int32 [B+1], nullable (no biases): row b has the */
+    const int32_t *bias_tokens;  /*   entries bias_begin[b] .. bias_begin[b+1]-1 of these   */
+    const float *bias_values;    /*   two device arrays of n_bias entries                   */
+    int n_bias;
+    const uint32_t *mask;        /* device [n_masks, W], nullable: bit 1 = token allowed */
+    int n_masks;
+    const int32_t *mask_index;   /* device int32 [B, P], nullable: the mask of (b, p), -1 for
+                                    none; NULL: mask b * P + p (n_masks = B * P) */
+} sv_logit_rules;
+
+/*
+ * sv_logits_process -- penalties for repeated tokens, biases and grammar masks
+ * on the logits of a block, position by position as sequential decoding
+ * would apply them, so that verifying the processed logits emits tokens
+ * distributed as the target under its rules.
+ *
+ * Position p of row b stands at i = pos0 + p of the block, behind the drafts
+ * x_0 .. x_{i-1}.  With c(v) = output_counts[v] + #{j < i : x_j = v} and
+ * seen(v) = c(v) > 0 or v in the prompt:
+ *   z1 = z / repetition if seen and z > 0;  z * repetition if seen;  else z
+ *   z2 = z1 - frequency * c - presence * [c > 0]
+ *   z3 = z2 + bias(v)
+ *   out = z3 where the mask allows v, -inf where it does not,
+ * in fp32, rounded once to `dtype`.  A forbidden logit is -inf whatever the
+ * logit was.  A bias of -inf bans its token; of a token listed twice the
+ * later entry counts.
+ *
+ *   logits, out    device [B, P, Vs] of `dtype`; out may be logits (then
+ *                  only the logits that change are touched) or must not
+ *                  overlap it.  Positions at i >= lengths[b] + extra are
+ *                  neither read nor written.
+ *   B, P           B >= 0; 1 <= P <= SV_MAX_K + 1.
+ *   V, v0, Vs      the vocabulary, and the slice [v0, v0 + Vs) that the
+ *                  logits hold (v0 = 0, Vs = V unsharded).  History, drafts,
+ *                  biases and masks are in tokens of the whole vocabulary.
+ *   draft_tokens   device int32 [B, K], nullable; K >= 0, at most SV_MAX_K.
+ *                  A draft outside [0, V) counts nowhere (SV_ROW_BAD_TOKEN).
+ *   pos0           block position of p = 0: 0 for a whole block, i for a
+ *                  drafter that processes its i-th position alone.
+ *   lengths        device int32 [B], nullable (every position); with
+ *                  sv_schedule's lengths, extra = 1 takes the target
+ *                  positions that sv_verify may read and extra = 0 the
+ *                  draft positions.
+ *   rules          HOST.  rules->history->V must equal V.  A row with an
+ *                  invalid penalty keeps it neutral (SV_ROW_BAD_PENALTY),
+ *                  an invalid slot reads an empty history, an invalid bias
+ *                  entry is left out (SV_ROW_BAD_TOKEN, SV_ROW_BAD_BIAS), an
+ *                  invalid mask index masks nothing.  A mask without an
+ *                  allowed token leaves only -inf and raises
+ *                  SV_ROW_EMPTY_MASK (detected only when `status` is given);
+ *                  sv_verify would emit token 0 with SV_NOTE_CDF_FALLBACK
+ *                  from such a position.
+ *   status         device int32, nullable; bits OR-ed in.
+ * Logit pointers must be aligned to their element size; vectors may start at
+ * any alignment.  One launch, no workspace.
+ * Returns SV_OK, SV_ERR_ARG, SV_ERR_SHAPE, SV_ERR_DTYPE or SV_ERR_CUDA.
+ */
+sv_status sv_logits_process(const void *logits, void *out, sv_dtype dtype, int B, int P, int V,
+                            int v0, int Vs, const int32_t *draft_tokens, int K, int pos0,
+                            const int32_t *lengths, int extra, const sv_logit_rules *rules,
+                            int32_t *status, void *stream);
+
+/*
+ * sv_head_w4 -- logits of an output head whose weights are held in 4 bits:
+ *
+ *   out[b, p, v] = sum_g scale[v, g] *
+ *                  sum_{k in group g} x[b, p, k] * (code[v, k] - zero[v, g]),
+ *
+ * for the last hidden states x of every scheduled position; sums in fp32, the
+ * products of a bf16 x and a 4-bit code exact, one rounding to out's type.
+ * The weights are read in the layout below, without a repacked copy.
+ */
+typedef struct {
+    const uint8_t *codes;    /* device [V, H / 2]: code k in the low (even k) or high (odd k)
+                                half of byte k / 2; 16-byte aligned */
+    const void *scale;       /* device [V, H / group] of scale_dtype */
+    const uint8_t *zero;     /* device [V, H / group], nullable (8): the low four bits count */
+    sv_dtype scale_dtype;    /* SV_F32 or SV_BF16 */
+    int V, H, group;         /* 1 <= V <= SV_MAX_V; group 32, 64 or 128; H a multiple of
+                                group, H <= SV_MAX_H */
+} sv_w4;
+
+#define SV_MAX_H 32768
+
+/*
+ *   x              device bf16 [B, P, H], 16-byte aligned.
+ *   out            device [B, P, V] of out_dtype (SV_F32 or SV_BF16).  Positions
+ *                  p >= lengths[b] + extra are neither computed nor written.
+ *   B, P           B >= 0, P >= 1, B * P <= 2^20.
+ *   lengths        device int32 [B], nullable (every position).
+ *   workspace      device scratch of sv_head_w4_workspace_bytes(weight, B, P)
+ *                  bytes, 16-byte aligned; may be NULL where that is 0.
+ *                  Calls that share a workspace must be stream-ordered.
+ * The same inputs give the same bits on every call.  Never synchronises.
+ * Returns SV_OK, SV_ERR_ARG, SV_ERR_SHAPE, SV_ERR_DTYPE, SV_ERR_WORKSPACE or
+ * SV_ERR_CUDA.  sv_head_w4_workspace_bytes returns 0 for unsupported sizes.
+ */
+size_t sv_head_w4_workspace_bytes(const sv_w4 *weight, int B, int P);
+sv_status sv_head_w4(const sv_w4 *weight, const void *x, int B, int P, const int32_t *lengths,
+                     int extra, void *out, sv_dtype out_dtype, void *workspace,
+                     size_t workspace_bytes, void *stream);
 
 /*
  * sv_philox_uniforms -- the uniforms sv_verify draws, for tests:

@@ -12,6 +12,9 @@ import torch
 SV_F32, SV_BF16 = 0, 1
 SV_ROW_BAD_TOKEN, SV_ROW_BAD_LENGTH, SV_ROW_BAD_TEMPERATURE = 1, 2, 4
 SV_NOTE_ZERO_RESIDUAL, SV_NOTE_CDF_FALLBACK = 8, 16
+SV_ROW_BAD_SLOT, SV_ROW_BAD_PENALTY, SV_ROW_BAD_BIAS = 64, 128, 256
+SV_ROW_BAD_MASK, SV_ROW_EMPTY_MASK = 512, 1024
+SV_HISTORY_PROMPT, SV_HISTORY_OUTPUT = 0, 1
 _STATUS = {0: "SV_OK", 1: "SV_ERR_ARG", 2: "SV_ERR_SHAPE", 3: "SV_ERR_DTYPE",
            4: "SV_ERR_WORKSPACE", 5: "SV_ERR_CUDA"}
 
@@ -77,6 +80,14 @@ def lib():
     L.sv_verify_host_workspace_bytes.restype = sz
     L.sv_verify_host.argtypes = [vp, vp, i32, i32, i32, i32, vp, ctypes.c_float, vp, vp, u64, i64,
                                  vp, vp, vp, vp, i32, vp, sz, vp, vp]
+    hp, rp, wp = (ctypes.POINTER(t) for t in (_History, _Rules, _W4))
+    L.sv_history_reset.argtypes = [hp, vp, i32, vp, vp]
+    L.sv_history_add.argtypes = [hp, vp, i32, vp, i32, vp, i32, i32, vp, vp]
+    L.sv_logits_process.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, vp, i32, i32, vp, i32,
+                                    rp, vp, vp]
+    L.sv_head_w4_workspace_bytes.argtypes = [wp, i32, i32]
+    L.sv_head_w4_workspace_bytes.restype = sz
+    L.sv_head_w4.argtypes = [wp, vp, i32, i32, vp, i32, vp, i32, vp, sz, vp]
     L.sv_philox_uniforms.argtypes = [u64, vp, vp, vp, i32, vp, vp]
     L.sv_philox4x32_10.argtypes = [vp, vp, i32, vp, vp]
     L.sv_profile_begin.argtypes = [i32]
@@ -89,7 +100,8 @@ def lib():
                  "sv_vp_decide",
                  "sv_vp_draw",
                  "sv_philox_uniforms",
-                 "sv_philox4x32_10", "sv_profile_begin"):
+                 "sv_philox4x32_10", "sv_profile_begin", "sv_history_reset", "sv_history_add",
+                 "sv_logits_process", "sv_head_w4"):
         getattr(L, name).restype = i32
     L.sv_last_cuda_error.restype = i32
     L.sv_version.restype = i32
@@ -369,6 +381,227 @@ def sv_verify_host(target_logits, draft_logits, conf, load: float, draft_tokens,
         workspace.numel() * workspace.element_size(), ctypes.byref(h2d),
         _stream(stream, workspace)))
     return int(h2d.value)
+
+
+# ---------------------------------------------------------------------------
+# Token history, logit rules, 4-bit head.
+# ---------------------------------------------------------------------------
+class _History(ctypes.Structure):
+    _fields_ = [("prompt_bits", ctypes.c_void_p), ("output_bits", ctypes.c_void_p),
+                ("output_counts", ctypes.c_void_p), ("R", ctypes.c_int), ("V", ctypes.c_int)]
+
+
+class _Rules(ctypes.Structure):
+    _fields_ = [("history", ctypes.POINTER(_History)), ("slots", ctypes.c_void_p),
+                ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+                ("presence", ctypes.c_void_p), ("bias_begin", ctypes.c_void_p),
+                ("bias_tokens", ctypes.c_void_p), ("bias_values", ctypes.c_void_p),
+                ("n_bias", ctypes.c_int), ("mask", ctypes.c_void_p), ("n_masks", ctypes.c_int),
+                ("mask_index", ctypes.c_void_p)]
+
+
+class _W4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p),
+                ("scale_dtype", ctypes.c_int), ("V", ctypes.c_int), ("H", ctypes.c_int),
+                ("group", ctypes.c_int)]
+
+
+def _given(t, dtype, name: str, like: torch.Tensor, shape=None):
+    """An optional tensor argument on the device of `like`: its address, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor")
+    if t.device != like.device:
+        raise TypeError(f"{name} must be on {like.device}, is on {t.device}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise TypeError(f"{name} must have the shape {shape}, has {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _call(fn: str, like: torch.Tensor, stream, *args) -> None:
+    """Call `fn` on the device of `like`, with the stream as the last argument."""
+    if not like.is_cuda:
+        raise TypeError(f"{fn}: the tensors must be on a GPU")
+    st = _stream(stream, like)
+    if like.device.index == torch.cuda.current_device():
+        _check(fn, getattr(lib(), fn)(*args, st))
+    else:
+        with torch.cuda.device(like.device):
+            _check(fn, getattr(lib(), fn)(*args, st))
+
+
+class TokenHistory:
+    """``sv_history``: the bit planes [R, ceil(V / 32)] (int32 words) and counts
+    [R, V] (int32) of R slots.  Holds its tensors; zero-filled ones are empty."""
+
+    def __init__(self, V: int, prompt_bits, output_bits, output_counts):
+        R, W = output_counts.shape[0], (V + 31) // 32
+        at = [_given(t, torch.int32, name, output_counts, shape) for name, t, shape in (
+            ("prompt_bits", prompt_bits, (R, W)), ("output_bits", output_bits, (R, W)),
+            ("output_counts", output_counts, (R, V)))]
+        self.prompt_bits, self.output_bits = prompt_bits, output_bits
+        self.output_counts = output_counts
+        self.R, self.V = R, V
+        self.desc = _History(*at, R, V)
+
+    @classmethod
+    def empty(cls, R: int, V: int, device) -> "TokenHistory":
+        planes = torch.zeros(2, R, (V + 31) // 32, dtype=torch.int32, device=device)
+        return cls(V, planes[0], planes[1],
+                   torch.zeros(R, V, dtype=torch.int32, device=device))
+
+
+class LogitRules:
+    """``sv_logit_rules``: every part may be None.  Per-row tensors have B
+    entries; biases are B lists, row b the entries bias_begin[b] ..
+    bias_begin[b + 1] - 1; mask is [n, ceil(V / 32)] int32 words, bit 1 =
+    allowed, and mask_index [B, P] names each position's mask (-1: none)."""
+
+    def __init__(self, history: Optional[TokenHistory] = None, slots=None, repetition=None,
+                 frequency=None, presence=None, bias_begin=None, bias_tokens=None,
+                 bias_values=None, mask=None, mask_index=None):
+        f32, i32 = torch.float32, torch.int32
+        rows = (("slots", slots, i32), ("repetition", repetition, f32),
+                ("frequency", frequency, f32), ("presence", presence, f32))
+        given = [t for _, t, _ in rows] + [bias_begin, mask, mask_index]
+        given += [] if history is None else [history.output_counts]
+        like = next((t for t in given if t is not None), None)
+        n = None
+        at = []
+        for name, t, dtype in rows:
+            at.append(_given(t, dtype, name, like))
+            if t is not None:
+                if t.dim() != 1 or n not in (None, t.numel()):
+                    raise TypeError("the per-row tensors must be vectors of the same length")
+                n = t.numel()
+        if history is not None:
+            _given(history.output_counts, i32, "history", like)
+        if (bias_begin is None) != (bias_tokens is None) or \
+                (bias_begin is None) != (bias_values is None):
+            raise TypeError("bias_begin, bias_tokens and bias_values go together")
+        n_bias = 0
+        if bias_begin is not None:
+            n_bias = bias_tokens.numel()
+            if n not in (None, bias_begin.numel() - 1):
+                raise TypeError("bias_begin must have one entry more than there are rows")
+            n = bias_begin.numel() - 1
+        at += [_given(bias_begin, i32, "bias_begin", like),
+               _given(bias_tokens, i32, "bias_tokens", like, (n_bias,)),
+               _given(bias_values, f32, "bias_values", like, (n_bias,))]
+        n_masks = 0
+        if mask is not None:
+            if mask.dim() != 2:
+                raise TypeError("mask must be [n, ceil(V / 32)]")
+            n_masks = mask.shape[0]
+        elif mask_index is not None:
+            raise TypeError("mask_index needs a mask")
+        self.rows, self.n_masks = n, n_masks
+        self.words = None if mask is None else mask.shape[1]
+        self.index_shape = None if mask_index is None else tuple(mask_index.shape)
+        self.history, self.device = history, None if like is None else like.device
+        self._keep = (slots, repetition, frequency, presence, bias_begin, bias_tokens,
+                      bias_values, mask, mask_index)
+        self.desc = _Rules(None if history is None else ctypes.pointer(history.desc), *at, n_bias,
+                           _given(mask, i32, "mask", like), n_masks,
+                           _given(mask_index, i32, "mask_index", like))
+
+
+class W4Weight:
+    """``sv_w4``: codes [V, H / 2] uint8 (even k in the low half of a byte),
+    scale [V, H / group] float32 or bfloat16, zero [V, H / group] uint8 or
+    None (8).  Holds its tensors."""
+
+    def __init__(self, codes, scale, zero=None):
+        V, H, G = codes.shape[0], 2 * codes.shape[1], scale.shape[1]
+        if G < 1 or H % G:
+            raise TypeError("scale must be [V, H / group] for codes [V, H / 2]")
+        at = (_given(codes, torch.uint8, "codes", codes),
+              _given(scale, torch.float32 if scale.dtype == torch.float32 else torch.bfloat16,
+                     "scale", codes, (V, G)),
+              _given(zero, torch.uint8, "zero", codes, (V, G)))
+        self.codes, self.scale, self.zero = codes, scale, zero
+        self.V, self.H, self.group = V, H, H // G
+        self.desc = _W4(*at, SV_F32 if scale.dtype == torch.float32 else SV_BF16, V, H, H // G)
+
+
+def sv_history_reset(history: TokenHistory, slots=None, n: Optional[int] = None, status=None,
+                     stream=None) -> None:
+    """Empty the listed slots, or the first n (default: all)."""
+    like = history.output_counts
+    if slots is not None:
+        n = slots.numel()
+    elif n is None:
+        n = history.R
+    _call("sv_history_reset", like, stream, history.desc,
+          _given(slots, torch.int32, "slots", like), int(n),
+          _given(status, torch.int32, "status", like))
+
+
+def sv_history_add(history: TokenHistory, tokens, lens=None, kind: int = SV_HISTORY_OUTPUT,
+                   slots=None, extra: int = 0, status=None, stream=None) -> None:
+    """Append the first lens[b] + extra (default: all) tokens of each row of
+    tokens [B, S]; sv_verify's results go in as tokens = out_tokens,
+    lens = out_accept_len, extra = 1."""
+    like = history.output_counts
+    B, S = tokens.shape
+    _call("sv_history_add", like, stream, history.desc,
+          _given(slots, torch.int32, "slots", like, (B,)), B,
+          _given(tokens, torch.int32, "tokens", like), S,
+          _given(lens, torch.int32, "lens", like, (B,)), int(extra), int(kind),
+          _given(status, torch.int32, "status", like))
+
+
+def sv_logits_process(logits, out, rules: LogitRules, draft_tokens=None, lengths=None,
+                      extra: int = 0, pos0: int = 0, V: Optional[int] = None, v0: int = 0,
+                      status=None, stream=None) -> None:
+    """Apply `rules` to logits [B, P, Vs] into `out` (which may be `logits`);
+    V and v0 place a vocabulary slice (default: the whole vocabulary)."""
+    B, P, Vs = logits.shape
+    dt = _dtype(logits)
+    V = Vs if V is None else int(V)
+    if rules.device is not None and rules.device != logits.device:
+        raise TypeError(f"the rules must be on {logits.device}, are on {rules.device}")
+    if rules.rows not in (None, B):
+        raise TypeError(f"the rules are for {rules.rows} rows, the logits have {B}")
+    if rules.words not in (None, (V + 31) // 32):
+        raise TypeError(f"mask must have {(V + 31) // 32} words a row, has {rules.words}")
+    if rules.index_shape not in (None, (B, P)):
+        raise TypeError(f"mask_index must be [{B}, {P}], is {list(rules.index_shape)}")
+    K = 0
+    if draft_tokens is not None:
+        if draft_tokens.dim() != 2 or draft_tokens.shape[0] != B:
+            raise TypeError("draft_tokens must be [B, K]")
+        K = draft_tokens.shape[1]
+    _call("sv_logits_process", logits, stream,
+          _given(logits, logits.dtype, "logits", logits),
+          _given(out, logits.dtype, "out", logits, (B, P, Vs)), dt, B, P, V, int(v0), Vs,
+          _given(draft_tokens, torch.int32, "draft_tokens", logits), K, int(pos0),
+          _given(lengths, torch.int32, "lengths", logits, (B,)), int(extra), rules.desc,
+          _given(status, torch.int32, "status", logits))
+
+
+def sv_head_w4_workspace_bytes(weight: W4Weight, B: int, P: int) -> int:
+    return int(lib().sv_head_w4_workspace_bytes(weight.desc, B, P))
+
+
+def sv_head_w4(weight: W4Weight, x, out, workspace=None, lengths=None, extra: int = 0,
+               stream=None) -> None:
+    """out [B, P, V] (float32 or bfloat16) = x [B, P, H] (bfloat16) times the
+    4-bit weights; positions p >= lengths[b] + extra are left as they were."""
+    B, P, H = x.shape
+    if H != weight.H:
+        raise TypeError(f"x must be [B, P, {weight.H}]")
+    if weight.codes.device != x.device:
+        raise TypeError(f"the weights must be on {x.device}, are on {weight.codes.device}")
+    n = 0
+    if workspace is not None:
+        if not workspace.is_contiguous() or workspace.device != x.device:
+            raise TypeError(f"workspace must be contiguous memory on {x.device}")
+        n = workspace.numel() * workspace.element_size()
+    _call("sv_head_w4", x, stream, weight.desc, _given(x, torch.bfloat16, "x", x), B, P,
+          _given(lengths, torch.int32, "lengths", x, (B,)), int(extra),
+          _given(out, out.dtype, "out", x, (B, P, weight.V)), _dtype(out), _ptr(workspace), n)
 
 
 def sv_philox_uniforms(seed: int, row, pos, draw, out, stream=None) -> None:

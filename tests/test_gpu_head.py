@@ -1,0 +1,236 @@
+"""The 4-bit output head on the GPU against its plain 64-bit form, and the
+chain head -> rules -> verification -> history."""
+import numpy as np
+import pytest
+import torch
+
+import _plain_rules as plain
+import speculative_decoding_verification_93_b200 as sv
+from oracle import compare as ocompare
+
+pytestmark = pytest.mark.gpu
+
+DT = {"float32": torch.float32, "bfloat16": torch.bfloat16}
+
+
+class Head:
+    def __init__(self, H, V, group, zero, scale, seed):
+        rng = self.rng = np.random.default_rng(seed)
+        G = H // group
+        self.H, self.V, self.group = H, V, group
+        self.codes = rng.integers(0, 16, (V, H)).astype(np.uint8)
+        self.zero = rng.integers(0, 16, (V, G)).astype(np.uint8) if zero else None
+        self.scale = torch.from_numpy(rng.uniform(0.01, 0.1, (V, G)).astype(np.float32)).to(DT[scale])
+        packed = torch.from_numpy(self.codes[:, 0::2] | self.codes[:, 1::2] << 4).cuda()
+        # the high half of a zero's byte is not part of it
+        z = None if self.zero is None else torch.from_numpy(self.zero | 0xa0).cuda()
+        self.weight = sv.W4Weight(packed, self.scale.cuda(), z)
+
+    def want(self, x, dtype):
+        zero = self.zero if self.zero is not None else np.full(self.scale.shape, 8)
+        out, bound = plain.head(x.double().cpu().numpy().reshape(-1, self.H), self.codes,
+                                self.scale.double().numpy(), zero, self.group, dtype)
+        return out.reshape(*x.shape[:2], self.V), bound.reshape(*x.shape[:2], self.V)
+
+    def run(self, x, dtype, lengths=None, extra=0, stream=None):
+        B, P, _ = x.shape
+        n, pad = B * P * self.V, 64
+        buf = torch.full((n + 2 * pad,), 55.0, dtype=DT[dtype], device="cuda")
+        out = buf[pad + 1:pad + 1 + n].view(B, P, self.V)      # no 16-byte boundary
+        need = sv.sv_head_w4_workspace_bytes(self.weight, B, P)
+        ws = torch.full((need + 16,), 255, dtype=torch.uint8, device="cuda") if need else None
+        torch.cuda.synchronize()
+        sv.sv_head_w4(self.weight, x, out, None if ws is None else ws[:need], lengths=lengths,
+                      extra=extra, stream=stream)
+        torch.cuda.synchronize()
+        assert bool((buf[:pad + 1] == 55).all() and (buf[pad + 1 + n:] == 55).all())
+        assert ws is None or bool((ws[need:] == 255).all())
+        return out
+
+    def check(self, x, dtype, lengths=None, extra=0, **kw):
+        got = self.run(x, dtype, lengths, extra, **kw).double().cpu().numpy()
+        want, bound = self.want(x, dtype)
+        if lengths is not None:
+            for b, n in enumerate(lengths.tolist()):
+                want[b, max(0, n + extra):], bound[b, max(0, n + extra):] = 55.0, 0.0
+        plain.check(got, want, bound)
+
+    def x(self, B, P):
+        return torch.from_numpy(self.rng.normal(0, 1, (B, P, self.H)).astype(np.float32)).to(
+            "cuda", torch.bfloat16)
+
+
+SHAPES = [(32, 1, 32), (64, 7, 32), (64, 8, 64), (128, 33, 128), (96, 100, 32), (256, 129, 64),
+          (1120, 1000, 32), (4096, 257, 128), (2048 + 64, 300, 64), (1408, 515, 128)]
+
+
+@pytest.mark.parametrize("H,V,group", SHAPES)
+@pytest.mark.parametrize("zero,scale", [(False, "bfloat16"), (True, "float32")])
+def test_head(H, V, group, zero, scale):
+    h = Head(H, V, group, zero, scale, seed=H + V)
+    for B, P in ((1, 1), (1, 2), (3, 1), (1, 5), (1, 8), (3, 3), (2, 8), (17, 1)):
+        for dtype in ("float32", "bfloat16"):
+            h.check(h.x(B, P), dtype)
+
+
+@pytest.mark.parametrize("M", [24, 31, 32, 33, 48, 63, 64, 65, 80, 96, 127, 128, 129, 255, 256, 257, 320,
+                               600])
+@pytest.mark.parametrize("H,V,group,zero", [(256, 300, 64, False), (1120, 131, 32, True),
+                                            (1024, 260, 128, True)])
+def test_head_many_tokens(M, H, V, group, zero):
+    h = Head(H, V, group, zero, "bfloat16", seed=M)
+    for dtype in ("float32", "bfloat16"):
+        h.check(h.x(M, 1), dtype)
+
+
+@pytest.mark.parametrize("B,P", [(1, 1), (5, 4), (40, 5), (3, 9)])
+def test_head_leaves_unscheduled_positions_as_they_were(B, P):
+    h = Head(512, 1031, 128, True, "bfloat16", seed=B)
+    for extra in (0, 1):
+        lengths = torch.from_numpy(h.rng.integers(-2, P + 2, B).astype(np.int32)).cuda()
+        x = h.x(B, P)
+        for b, n in enumerate(lengths.tolist()):
+            x[b, max(0, n + extra):] = float("nan")            # never read into another row
+        h.check(x, "bfloat16", lengths, extra)
+        none = torch.full((B,), -1, dtype=torch.int32, device="cuda")
+        h.check(x, "float32", none, extra)
+
+
+@pytest.mark.parametrize("M", [3, 9, 40, 130])
+def test_head_infinities_stay_in_their_row(M):
+    h = Head(256, 140, 64, False, "float32", seed=M)
+    x = h.x(M, 1)
+    x[1, 0, 5], x[2, 0, 250] = float("inf"), float("nan")
+    got = h.run(x, "float32").double().cpu().numpy()
+    want, bound = h.want(x.nan_to_num(0, 0, 0), "float32")
+    clean = [t for t in range(M) if t not in (1, 2)]
+    plain.check(got[clean], want[clean], bound[clean])
+    assert np.isnan(got[2]).all() and not np.isfinite(got[1]).any()
+
+
+def test_head_same_bits_every_time():
+    h = Head(1024, 700, 128, False, "bfloat16", seed=3)
+    for M in (1, 9, 70):
+        x = h.x(M, 1)
+        first = h.run(x, "float32")
+        for _ in range(3):
+            assert torch.equal(h.run(x, "float32"), first)
+
+
+def test_head_on_streams_and_in_a_graph():
+    h = Head(512, 2000, 64, True, "bfloat16", seed=9)
+    for M in (1, 20, 140):
+        xs = [h.x(M, 1) for _ in range(2)]
+        want = [h.want(x, "float32") for x in xs]
+        outs = [torch.zeros(M, 1, 2000, device="cuda") for _ in xs]
+        need = sv.sv_head_w4_workspace_bytes(h.weight, M, 1)
+        ws = [torch.empty(max(need, 16), dtype=torch.uint8, device="cuda") for _ in xs]
+        streams = [torch.cuda.Stream() for _ in xs]
+        torch.cuda.synchronize()
+        for i, s in enumerate(streams):
+            sv.sv_head_w4(h.weight, xs[i], outs[i], ws[i], stream=s)
+        torch.cuda.synchronize()
+        for i in range(2):
+            plain.check(outs[i].double().cpu().numpy(), *want[i])
+        # two graphs that share a workspace, replayed one after the other
+        graphs = []
+        for i in range(2):
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[i]):
+                sv.sv_head_w4(h.weight, xs[i], outs[i], ws[0])
+        for _ in range(2):
+            for o in outs:
+                o.zero_()
+            for g in graphs:
+                g.replay()
+            torch.cuda.synchronize()
+            for i in range(2):
+                plain.check(outs[i].double().cpu().numpy(), *want[i])
+
+
+def test_head_refuses_a_short_workspace():
+    h = Head(4096, 1000, 128, False, "bfloat16", seed=1)
+    for M in (1, 100):
+        need = sv.sv_head_w4_workspace_bytes(h.weight, M, 1)
+        if need == 0:
+            continue
+        x, out = h.x(M, 1), torch.zeros(M, 1, 1000, device="cuda")
+        with pytest.raises(sv.SVError) as e:
+            sv.sv_head_w4(h.weight, x, out, torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+        assert e.value.code == 4
+        with pytest.raises(sv.SVError) as e:
+            sv.sv_head_w4(h.weight, x, out)
+        assert e.value.code == 1
+
+
+@pytest.mark.parametrize("B,K,V,seed", [(4, 4, 1000, 0), (9, 3, 2051, 1), (64, 5, 1500, 2)])
+def test_head_rules_verification_and_history_together(B, K, V, seed):
+    """Two decoding steps of a small model: the target's and the drafter's
+    heads, the rules of every request, verification, and the history that
+    the second step's penalties read.  Verification is checked against the
+    oracle on the processed logits themselves."""
+    rng = np.random.default_rng(seed)
+    target, drafter = Head(256, V, 64, True, "bfloat16", seed), Head(128, V, 32, False, "float32", seed + 1)
+    history, plain_history = sv.TokenHistory.empty(B, V, "cuda"), plain.History(B, V)
+    dev = lambda x: torch.as_tensor(np.ascontiguousarray(x)).cuda()  # noqa: E731
+    rep, freq, pres = (rng.uniform(lo, hi, B).astype(np.float32)
+                       for lo, hi in ((1.0, 1.5), (0, 0.4), (0, 0.4)))
+    ban = rng.integers(0, V, B).astype(np.int32)
+    temp = rng.choice([0.0, 0.7, 1.0], B).astype(np.float32)
+    prompt = rng.integers(0, V, (B, 30)).astype(np.int32)
+    sv.sv_history_add(history, dev(prompt), kind=sv.SV_HISTORY_PROMPT)
+    for b in range(B):
+        plain_history.add(b, prompt[b], prompt=True)
+    for step in range(2):
+        allowed = rng.random((B, K + 1, V)) < np.where(np.arange(B) % 3 == 0, 0.3, 1.0)[:, None, None]
+        drafts = rng.integers(0, V, (B, K)).astype(np.int32)
+        drafts[1 % B] = drafts[1 % B, 0]
+        for i in range(K):                     # drafts come from the grammar
+            allowed[np.arange(B), i, drafts[:, i]] = True
+        lengths = rng.integers(0, K + 1, B).astype(np.int32)
+        rules = dict(history=history, repetition=dev(rep), frequency=dev(freq), presence=dev(pres),
+                     bias_begin=dev(np.arange(B + 1, dtype=np.int32)), bias_tokens=dev(ban),
+                     bias_values=dev(np.full(B, -3.0, np.float32)))
+        words = plain.pack(allowed)
+        on_target = sv.LogitRules(**rules, mask=dev(words.reshape(B * (K + 1), -1)))
+        on_draft = sv.LogitRules(**rules, mask=dev(words[:, :K].reshape(B * K, -1)))
+        xt, xd = target.x(B, K + 1), drafter.x(B, K)
+        ln, dr = dev(lengths), dev(drafts)
+        zt = torch.full((B, K + 1, V), 9.0, device="cuda")
+        zd = torch.full((B, K, V), 9.0, device="cuda")
+        ws = torch.empty(max(16, sv.sv_head_w4_workspace_bytes(target.weight, B, K + 1),
+                             sv.sv_head_w4_workspace_bytes(drafter.weight, B, K)),
+                         dtype=torch.uint8, device="cuda")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        sv.sv_head_w4(target.weight, xt, zt, ws, lengths=ln, extra=1)
+        sv.sv_head_w4(drafter.weight, xd, zd, ws, lengths=ln)
+        raw = zt.clone(), zd.clone()
+        sv.sv_logits_process(zt, zt, on_target, dr, ln, extra=1, status=st)
+        sv.sv_logits_process(zd, zd, on_draft, dr, ln, status=st)
+        tokens, accepted = sv.verify(zt, zd, dr, ln, dev(temp), seed=77 + step, status=st)
+        sv.sv_history_add(history, tokens, accepted, extra=1, status=st)
+        torch.cuda.synchronize()
+        assert int(st) & ~(sv.SV_NOTE_CDF_FALLBACK | sv.SV_NOTE_ZERO_RESIDUAL) == 0
+        bias = [{int(t): -3.0} for t in ban]
+        for b in range(B):                     # the logits that verification saw
+            for z, before, extra in ((zt, raw[0], 1), (zd, raw[1], 0)):
+                n = int(lengths[b]) + extra
+                if n == 0:
+                    continue
+                want, bound = plain.process(
+                    before[b].double().cpu().numpy(), "float32", drafts[b], 0, n,
+                    plain_history.prompt[b], plain_history.counts[b], float(rep[b]), float(freq[b]),
+                    float(pres[b]), bias[b], list(allowed[b]))
+                plain.check(z[b].double().cpu().numpy(), want, bound)
+        zt_h, zd_h = zt.cpu().numpy(), zd.cpu().numpy()
+        tally = ocompare.check_rows(lambda idx: (zt_h[idx], zd_h[idx]), drafts, temp, 77 + step,
+                                    lengths, lengths, lengths, lengths, tokens.cpu().numpy(),
+                                    accepted.cpu().numpy())
+        assert tally.invalid == 0, tally.first_invalid
+        tok, acc = tokens.cpu().numpy(), accepted.cpu().numpy()
+        for b in range(B):
+            emitted = tok[b, :acc[b] + 1]
+            assert all(allowed[b, i, t] for i, t in enumerate(emitted))
+            plain_history.add(b, emitted)
+        assert np.array_equal(history.output_counts.cpu().numpy(), plain_history.counts)
+        assert np.array_equal(history.output_bits.cpu().numpy(), plain.pack(plain_history.counts > 0))
