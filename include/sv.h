@@ -707,8 +707,11 @@ typedef struct {
  *   B, P           B >= 0, P >= 1, B * P <= 2^20.
  *   lengths        device int32 [B], nullable (every position).
  *   workspace      device scratch of sv_head_w4_workspace_bytes(weight, B, P)
- *                  bytes, 16-byte aligned; may be NULL where that is 0.
- *                  Calls that share a workspace must be stream-ordered.
+ *                  bytes, 16-byte aligned: the scheduled tokens of x in the
+ *                  matrix unit's layout.  Calls that share a workspace must
+ *                  be stream-ordered.
+ *   status         device int32, nullable; SV_NOTE_TIMEOUT is OR-ed in if an
+ *                  internal wait ran out (out is then undefined).
  * The same inputs give the same bits on every call.  Never synchronises.
  * Returns SV_OK, SV_ERR_ARG, SV_ERR_SHAPE, SV_ERR_DTYPE, SV_ERR_WORKSPACE or
  * SV_ERR_CUDA.  sv_head_w4_workspace_bytes returns 0 for unsupported sizes.
@@ -716,7 +719,7 @@ typedef struct {
 size_t sv_head_w4_workspace_bytes(const sv_w4 *weight, int B, int P);
 sv_status sv_head_w4(const sv_w4 *weight, const void *x, int B, int P, const int32_t *lengths,
                      int extra, void *out, sv_dtype out_dtype, void *workspace,
-                     size_t workspace_bytes, void *stream);
+                     size_t workspace_bytes, int32_t *status, void *stream);
 
 /*
  * sv_philox_uniforms -- the uniforms sv_verify draws, for tests:

@@ -87,7 +87,7 @@ def lib():
                                     rp, vp, vp]
     L.sv_head_w4_workspace_bytes.argtypes = [wp, i32, i32]
     L.sv_head_w4_workspace_bytes.restype = sz
-    L.sv_head_w4.argtypes = [wp, vp, i32, i32, vp, i32, vp, i32, vp, sz, vp]
+    L.sv_head_w4.argtypes = [wp, vp, i32, i32, vp, i32, vp, i32, vp, sz, vp, vp]
     L.sv_philox_uniforms.argtypes = [u64, vp, vp, vp, i32, vp, vp]
     L.sv_philox4x32_10.argtypes = [vp, vp, i32, vp, vp]
     L.sv_profile_begin.argtypes = [i32]
@@ -585,7 +585,7 @@ def sv_head_w4_workspace_bytes(weight: W4Weight, B: int, P: int) -> int:
     return int(lib().sv_head_w4_workspace_bytes(weight.desc, B, P))
 
 
-def sv_head_w4(weight: W4Weight, x, out, workspace=None, lengths=None, extra: int = 0,
+def sv_head_w4(weight: W4Weight, x, out, workspace, lengths=None, extra: int = 0, status=None,
                stream=None) -> None:
     """out [B, P, V] (float32 or bfloat16) = x [B, P, H] (bfloat16) times the
     4-bit weights; positions p >= lengths[b] + extra are left as they were."""
@@ -594,14 +594,12 @@ def sv_head_w4(weight: W4Weight, x, out, workspace=None, lengths=None, extra: in
         raise TypeError(f"x must be [B, P, {weight.H}]")
     if weight.codes.device != x.device:
         raise TypeError(f"the weights must be on {x.device}, are on {weight.codes.device}")
-    n = 0
-    if workspace is not None:
-        if not workspace.is_contiguous() or workspace.device != x.device:
-            raise TypeError(f"workspace must be contiguous memory on {x.device}")
-        n = workspace.numel() * workspace.element_size()
     _call("sv_head_w4", x, stream, weight.desc, _given(x, torch.bfloat16, "x", x), B, P,
           _given(lengths, torch.int32, "lengths", x, (B,)), int(extra),
-          _given(out, out.dtype, "out", x, (B, P, weight.V)), _dtype(out), _ptr(workspace), n)
+          _given(out, out.dtype, "out", x, (B, P, weight.V)), _dtype(out),
+          _given(workspace, workspace.dtype, "workspace", x),
+          workspace.numel() * workspace.element_size(),
+          _given(status, torch.int32, "status", x))
 
 
 def sv_philox_uniforms(seed: int, row, pos, draw, out, stream=None) -> None:

@@ -100,7 +100,7 @@ def _head(weight=None, **kw):
         (w if k in w else d)[k] = v
     w = bd._W4(*(w[n] for n, _ in bd._W4._fields_))
     return sv.lib().sv_head_w4(w, d["x"], d["B"], d["P"], d["lengths"], d["extra"], d["out"],
-                               d["out_dtype"], d["ws"], d["wsb"], None)
+                               d["out_dtype"], d["ws"], d["wsb"], None, None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -108,6 +108,7 @@ def _head(weight=None, **kw):
     (dict(codes=A[0] + 8), ARG), (dict(x=A[1] + 2), ARG), (dict(scale=A[4] + 1), ARG),
     (dict(scale_dtype=sv.SV_F32, scale=A[4] + 2), ARG), (dict(out=A[2] + 1), ARG),
     (dict(out_dtype=sv.SV_F32, out=A[2] + 2), ARG), (dict(ws=A[3] + 8), ARG),
+    (dict(ws=None), ARG), (dict(wsb=1000), WORKSPACE),
     (dict(out_dtype=2), DTYPE), (dict(scale_dtype=7), DTYPE),
     (dict(V=0), SHAPE), (dict(V=(1 << 20) + 1), SHAPE), (dict(H=0), SHAPE), (dict(H=96), SHAPE),
     (dict(group=16), SHAPE), (dict(group=256), SHAPE), (dict(H=32768 + 64), SHAPE),
@@ -156,9 +157,9 @@ def test_binding_refuses():
     w = sv.W4Weight(codes, torch.zeros(7, 2))
     assert (w.V, w.H, w.group) == (7, 128, 64)
     with pytest.raises(TypeError, match="x must be"):
-        sv.sv_head_w4(w, torch.zeros(1, 1, 64, dtype=torch.bfloat16), torch.zeros(1, 1, 7))
+        sv.sv_head_w4(w, torch.zeros(1, 1, 64, dtype=torch.bfloat16), torch.zeros(1, 1, 7), z)
     with pytest.raises(TypeError, match="out"):
-        sv.sv_head_w4(w, torch.zeros(1, 1, 128, dtype=torch.bfloat16), torch.zeros(1, 2, 7))
+        sv.sv_head_w4(w, torch.zeros(1, 1, 128, dtype=torch.bfloat16), torch.zeros(1, 2, 7), z)
 
 
 def test_plain_bit_planes_round_trip():
