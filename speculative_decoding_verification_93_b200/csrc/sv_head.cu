@@ -16,14 +16,14 @@
 // walks 128-row tiles of the vocabulary, K in stages of 128:
 //   warp 0      copies the stage's x image into a ring of shared memory
 //               (bulk copies, mbarrier completion);
-//   warps 4-7   own one weight row per thread: codes arrive through a ring of
-//               asynchronous 16-byte copies, are widened to bf16 integers
-//               (one logic operation and one exact subtraction for two
-//               codes) and written to tensor memory as the A operand;
-//   warp 1      one thread issues tcgen05.mma, A from tensor memory, B from
-//               shared memory, one batch per (group, half of the tokens);
-//   warps 8-15  one warpgroup per half of the tokens reads each finished
-//               batch back, scales and accumulates it, and writes the logits.
+//   warps 2, 3  fetch scales and zero points into a ring of their own;
+//   one or two warpgroups own one weight row per thread: codes arrive
+//               through a ring of asynchronous 16-byte copies, are widened to
+//               bf16 integers and written to tensor memory as the A operand;
+//   warp 1      issues tcgen05.mma, A from tensor memory, B from shared
+//               memory, one batch per (group, half of the tokens);
+//   two warpgroups, one per half of the tokens, read each finished batch
+//               back, scale and accumulate it, and write the logits.
 // The two halves alternate, so the matrix unit works on one half while the
 // other is read back.  A in tensor memory keeps the widened weights (four
 // times the bytes of the codes) out of shared memory, whose bandwidth the B
@@ -184,7 +184,6 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
@@ -205,6 +204,14 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&f)[16]) {
         : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7]),
           "=f"(f[8]), "=f"(f[9]), "=f"(f[10]), "=f"(f[11]), "=f"(f[12]), "=f"(f[13]), "=f"(f[14]), "=f"(f[15])
         : "r"(addr) : "memory");
+}
+// Loads from tensor memory land by the wait; naming their registers here
+// keeps every use behind it.
+__device__ __forceinline__ void tc_wait_ld(float (&f)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3]), "+f"(f[4]), "+f"(f[5]), "+f"(f[6]), "+f"(f[7]),
+                   "+f"(f[8]), "+f"(f[9]), "+f"(f[10]), "+f"(f[11]), "+f"(f[12]), "+f"(f[13]), "+f"(f[14]), "+f"(f[15])
+                 :: "memory");
 }
 template <int N> __device__ __forceinline__ void regs_less() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -231,30 +238,52 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
 // ---------------------------------------------------------------------------
 // 3. The product.
 // ---------------------------------------------------------------------------
-constexpr int kHeadThreads = 512;
-constexpr int kCodeSlots = 8;            // ring of code stages: 8 KB each
+constexpr int kStageBytes = kTileV * kStageK / 2;   // codes of one stage
 constexpr int kASlots = 4;               // A operands in tensor memory: 64 columns each
 constexpr int kACol = 256;               // behind the accumulators
 constexpr uint32_t kTmemCols = 512;
+constexpr int kParGroups = 8;            // groups per chunk of the parameter ring
+constexpr int kParSlots = 3;
 constexpr uint64_t kHeadWaitNs = 1000000000ull;
 
+// Scale and zero point of kParGroups groups of a tile's rows.  `off` is the
+// pair -zero / 64 in bf16 (see widen8).
+struct ParChunk {
+    float scale[kParGroups][kTileV];
+    uint32_t off[kParGroups][kTileV];
+};
+
 // Per instantiation: up to NH tokens a half, DB accumulators per half, XS
-// stages of x.
+// stages of x, CS stages of codes, WW warpgroups that widen codes.
+// One warpgroup widens a stage in about 400 cycles (latency; 200 of issue),
+// the copies of a stage's codes take 350, and the matrix unit 8 nh cycles:
+// above 64 tokens a half one is enough, and the accumulators need the
+// registers of the second.
 template <int NH> struct HeadCfg {
-    static constexpr int DB = NH <= 64 ? 2 : 1;
-    static constexpr int XS = NH <= 16 ? 8 : NH <= 64 ? 4 : 2;
+    static constexpr int DB = NH <= 16 ? 4 : NH <= 64 ? 2 : 1;
+    static constexpr int XS = NH <= 16 ? 8 : NH <= 64 ? 3 : 2;
+    static constexpr int CS = NH <= 64 ? 12 : 8;
+    static constexpr int WW = NH <= 64 ? 2 : 1;
+    static constexpr int kThreads = 128 * (3 + WW);
+    // Registers a thread of the service, widening and accumulating
+    // warpgroups: their sum stays below what the CTA was launched with.
+    static constexpr int kRegs0 = 56, kRegsW = WW == 2 ? 80 : 88, kRegsA = WW == 2 ? 128 : 184;
+    static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+    static_assert(kRegs0 + WW * kRegsW + 2 * kRegsA <= (3 + WW) * kLaunchRegs, "register split");
     static constexpr int kXBytes = 2 * NH * 256;
-    static constexpr int kCodeBytes = kCodeSlots * kTileV * 64;
-    static constexpr int kUsed = 1024 + XS * kXBytes + kCodeBytes;
     // At least half of the SM's shared memory: two CTAs on one SM would
     // wait for each other's tensor memory.
+    static constexpr int kUsed = 1024 + XS * kXBytes + CS * kStageBytes +
+                                 kParSlots * static_cast<int>(sizeof(ParChunk));
     static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
+    static_assert(CS % WW == 0 && 2 * NH * DB <= kACol && kSmem <= 227 * 1024 - 1024, "head layout");
 };
 
 struct HeadBars {
     uint64_t xfull[8], xempty[8];
     uint64_t afull[kASlots], aempty[kASlots];
-    uint64_t dfull[4], dempty[4];
+    uint64_t dfull[8], dempty[8];
+    uint64_t pfull[kParSlots], pempty[kParSlots];
     uint64_t drain;
     uint32_t tmem;
 };
@@ -264,245 +293,426 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, kHeadWaitNs));
 }
 
-__device__ __forceinline__ float ld_scale(const HeadArgs &a, long long at) {
-    return a.scale_f32 ? __ldg(static_cast<const float *>(a.scale) + at)
-                       : ld_elem<2>(static_cast<const char *>(a.scale), at);
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
 }
 
-// Eight codes to four pairs of bf16 integers: 128 + code by one logic
-// operation (the ulp of bf16 in [128, 256) is 1), minus 128 + zero, exact.
-__device__ __forceinline__ void widen8(uint32_t w, __nv_bfloat162 off, uint32_t *r) {
+__device__ __forceinline__ int warp_value(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// Eight codes to four pairs (code - zero) / 64 in bf16, exact.  A code in the
+// low bits of a bf16 is the number code * 2^-133 (bits 0-3) or code * 2^-129
+// (bits 4-7): below the normal numbers, where the format is linear, up to
+// 2^-126 * 2.  So one mask takes out two codes, and one fused multiply-add by
+// 2^127 (2^123) subtracts the zero point with no exponent to set first: five
+// integer operations, which run at half the rate of the others, for eight
+// codes, against seven when 128 is OR-ed in.  The factor 64 is in the scale.
+__device__ __forceinline__ void widen8(uint32_t w, uint32_t off, uint32_t *r) {
+    const uint32_t h = w >> 8;
+    const uint32_t p[4] = {w & 0x000f000fu, w & 0x00f000f0u, h & 0x000f000fu, h & 0x00f000f0u};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t p = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&p), off);
-        r[i] = *reinterpret_cast<const uint32_t *>(&d);
-    }
+    for (int i = 0; i < 4; ++i)
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r[i]) : "r"(p[i]), "r"(i & 1 ? 0x7d007d00u : 0x7f007f00u), "r"(off));
 }
 
-// Warps 4-7.  GROUP is the weights' group.
-template <int GROUP>
-__device__ bool widen_role(const HeadArgs &a, HeadBars &bar, char *ring, uint32_t tmem, int passes) {
-    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
-    char *mine = ring + quarter * 32 * 64;              // this warp's 32 rows of a slot
-    constexpr int kSlot = kTileV * 64;
-    const long long row_bytes = a.H / 2;
-    const int tail_pieces = ((a.H % kStageK) ? (a.H % kStageK) : kStageK) / 32;
-    const int my_tiles = (a.tiles - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) /
-                         static_cast<int>(gridDim.x);
-    const int total = my_tiles * passes * a.nkb;   // stages of this CTA
-    int f_kb = 0, f_pass = 0, f_tile = blockIdx.x, f_s = 0;   // next stage to fetch
-    auto fetch = [&]() {
-        if (f_s < total) {
-            char *slot = mine + (f_s % kCodeSlots) * kSlot;
-            const int pieces = f_kb == a.nkb - 1 ? tail_pieces : 4;
-            const int j = lane & 3;
+__device__ __forceinline__ uint32_t zero_pair(uint32_t z) {
+    const __nv_bfloat162 p = __float2bfloat162_rn(static_cast<float>(z) * (-1.f / 64.f));   // exact
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+// The x images of every stage into shared memory (one lane of warp 0).
+template <int NH>
+__device__ bool copy_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars &bar, char *xring) {
+    using Cfg = HeadCfg<NH>;
+    const uint32_t bytes = t.per * 256;
+    bool ok = true;
+    int s = 0;
+    for (int job = 0; ok && job < jobs; ++job) {
+        const char *src = a.image + static_cast<long long>(job % t.passes) * a.nkb * bytes;
+        for (int kb = 0; kb < a.nkb; ++kb, ++s) {
+            const int slot = s % Cfg::XS;
+            if (!mbar_wait(&bar.xempty[slot], ((s / Cfg::XS) & 1) ^ 1, kHeadWaitNs)) { ok = false; break; }
+            mbar_arrive_expect_tx(&bar.xfull[slot], bytes);
+            bulk_g2s(xring + slot * Cfg::kXBytes, src + static_cast<long long>(kb) * bytes, bytes, &bar.xfull[slot]);
+        }
+    }
+    // The copies in flight land before this CTA may leave.
+    for (int q = max(0, s - Cfg::XS); q < s; ++q)
+        mbar_wait(&bar.xfull[q % Cfg::XS], (q / Cfg::XS) & 1, kHeadWaitNs);
+    return ok;
+}
+
+// The matrix unit's instructions (warp 1: every lane runs the loops, so that
+// the operands stay in uniform registers; one lane issues).
+template <int NH, int GROUP>
+__device__ bool mma_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars &bar, const char *xring,
+                         uint32_t tmem) {
+    using Cfg = HeadCfg<NH>;
+    constexpr int kSubs = kStageK / GROUP;
+    const uint32_t nh = warp_value(t.nh);
+    const int halves = warp_value(t.halves), stages = warp_value(jobs) * a.nkb;
+    const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((nh >> 3) << 17) | ((kTileV >> 4) << 24);
+    const uint64_t x0 = smem_desc(smem_u32(xring));
+    const bool issuer = elect_one();
+    int i = 0, kb = 0;                    // group (counts through all jobs), stage of the job
+    bool ok = true;
+    for (int s = 0; s < stages; ++s) {
+        const int ab = s % kASlots, slot = s % Cfg::XS;
+        if (!warp_wait(&bar.afull[ab], (s / kASlots) & 1) ||
+            !warp_wait(&bar.xfull[slot], (s / Cfg::XS) & 1)) { ok = false; break; }
+        const int subs = min(kSubs, (a.H - kb * kStageK) / GROUP);
+        const uint64_t xs = x0 + static_cast<uint64_t>(slot * (Cfg::kXBytes / 16));
+        const uint32_t acol = tmem + kACol + ab * 64;
+#pragma unroll
+        for (int g = 0; g < kSubs; ++g) {
+            if (g >= subs) break;
+            for (int h = 0; h < halves; ++h) {
+                const int db = h * Cfg::DB + i % Cfg::DB;
+                if (!warp_wait(&bar.dempty[db], ((i / Cfg::DB) & 1) ^ 1)) { ok = false; break; }
+                tc_fence_after();
+                if (issuer) {
+                    const uint64_t xh = xs + static_cast<uint64_t>(h * 2 * nh * 8);
+#pragma unroll
+                    for (int q = 0; q < GROUP / 16; ++q) {
+                        const int k16 = g * (GROUP / 16) + q;
+                        mma_ts(tmem + db * NH, acol + 8 * k16, xh + (k16 >> 2) * nh * 8 + (k16 & 3) * 2, idesc, q > 0);
+                    }
+                    mma_commit(&bar.dfull[db]);
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            ++i;
+        }
+        if (!ok) break;
+        if (issuer) {
+            mma_commit(&bar.aempty[ab]);
+            mma_commit(&bar.xempty[slot]);
+        }
+        __syncwarp();
+        if (++kb == a.nkb) kb = 0;
+    }
+    // Nothing of the matrix unit is in flight when tensor memory is freed.
+    if (issuer) mma_commit(&bar.drain);
+    __syncwarp();
+    warp_wait(&bar.drain, 0);
+    return ok;
+}
+
+// Scales and zero points (warps 2 and 3, two rows a lane): as fp32 and bf16
+// pairs in shared memory, eight groups at a time, so that the rows' strided
+// reads are 16 bytes wide where the alignment allows it, made once for both
+// halves, and far ahead of their use.
+__device__ bool param_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars &bar, ParChunk *ring) {
+    const int l = threadIdx.x & 63;       // warps 2 and 3
+    const bool wide = !a.scale_f32 && a.G % 8 == 0 && (reinterpret_cast<uintptr_t>(a.scale) & 15) == 0;
+    int c = 0;
+    for (int job = 0; job < jobs; ++job) {
+        const int tile = blockIdx.x + job / t.passes * gridDim.x;
+        for (int g0 = 0; g0 < a.G; g0 += kParGroups, ++c) {
+            float sc[2][kParGroups];
+            uint32_t zp[2][kParGroups];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const long long at = static_cast<long long>(min(tile * kTileV + r * 64 + l, a.V - 1)) * a.G + g0;
+                if (wide) {
+                    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.scale) + at));
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) { sc[r][2 * q] = bf16_lo(w[q]); sc[r][2 * q + 1] = bf16_hi(w[q]); }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < kParGroups; ++q) {
+                        const long long e = at + min(q, a.G - 1 - g0);
+                        sc[r][q] = a.scale_f32 ? __ldg(static_cast<const float *>(a.scale) + e)
+                                               : ld_elem<2>(static_cast<const char *>(a.scale), e);
+                    }
+                }
+                if (a.zero) {
+#pragma unroll
+                    for (int q = 0; q < kParGroups; ++q) zp[r][q] = __ldg(a.zero + at + min(q, a.G - 1 - g0)) & 15u;
+                }
+            }
+            ParChunk &p = ring[c % kParSlots];
+            if (!warp_wait(&bar.pempty[c % kParSlots], ((c / kParSlots) & 1) ^ 1)) return false;
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int q = 0; q < kParGroups; ++q) {
+                    p.scale[q][r * 64 + l] = 64.f * sc[r][q];
+                    if (a.zero) p.off[q][r * 64 + l] = zero_pair(zp[r][q]);
+                }
+            mbar_arrive(&bar.pfull[c % kParSlots]);
+        }
+    }
+    return true;
+}
+
+// One warpgroup of wi = 0 .. WW - 1: the stages s = wi mod WW, one weight row a
+// thread.  Codes come by asynchronous 16-byte copies, four lanes a row (64
+// contiguous bytes), each warp for its own 32 rows.
+template <int NH, int GROUP> struct Widen {
+    using Cfg = HeadCfg<NH>;
+    static constexpr int kRing = Cfg::CS / Cfg::WW;   // slots of this warpgroup
+    static constexpr int kSubs = kStageK / GROUP;
+    const HeadArgs &a;
+    char *mine;                           // this warp's rows of the warpgroup's first slot
+    int lane, quarter, wi;
+    int f_kb, f_pass, f_tile, f_n;        // next stage to fetch, stages fetched
+    const uint8_t *src[4];                // this lane's rows in the tile being fetched
+
+    __device__ Widen(const HeadArgs &args, char *ring, int wi_) : a(args), wi(wi_) {
+        lane = threadIdx.x & 31;
+        quarter = (threadIdx.x >> 5) & 3;
+        mine = ring + wi * kRing * kStageBytes + quarter * 32 * 64;
+        f_kb = wi; f_pass = 0; f_tile = blockIdx.x; f_n = 0;
+        aim();
+    }
+    __device__ __forceinline__ void aim() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const long long v = min(f_tile * kTileV + quarter * 32 + 8 * i + (lane >> 2), a.V - 1);
+            src[i] = a.codes + v * (a.H / 2) + (lane & 3) * 16;
+        }
+    }
+    // 32-code pieces of stage kb.
+    __device__ __forceinline__ int pieces(int kb) const { return min(4, a.H / 32 - 4 * kb); }
+    __device__ __forceinline__ void copy() {
+        char *slot = mine + (f_n % kRing) * kStageBytes;
+        if ((lane & 3) < pieces(f_kb)) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = 8 * i + (lane >> 2);
-                const long long v = min(f_tile * kTileV + quarter * 32 + r, a.V - 1);
-                if (j < pieces)
-                    cp_async16(slot + r * 64 + ((j ^ ((r >> 1) & 3)) * 16),
-                               a.codes + v * row_bytes + f_kb * 64 + j * 16);
-            }
-            ++f_s;
-            if (++f_kb == a.nkb) {
-                f_kb = 0;
-                if (++f_pass == passes) { f_pass = 0; f_tile += gridDim.x; }
+                cp_async16(slot + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) * 16), src[i] + f_kb * 64);
             }
         }
-        cp_async_commit();
-    };
+        ++f_n;
+        f_kb += Cfg::WW;
+    }
+    // The first stages of the first tile, whatever the token count.
+    __device__ void start() {
 #pragma unroll 1
-    for (int i = 0; i < kCodeSlots - 1; ++i) fetch();
-    int kb = 0, pass = 0, tile = blockIdx.x;
-    for (int s = 0; s < total; ++s) {
-        cp_async_wait<kCodeSlots - 2>();
-        __syncwarp();          // every lane's copies of stage s have landed; stage s - 1 is read
-        fetch();
-        const long long v = min(tile * kTileV + quarter * 32 + lane, a.V - 1);
-        const char *row = mine + (s % kCodeSlots) * kSlot + lane * 64;
-        const int pieces = kb == a.nkb - 1 ? tail_pieces : 4;
-        constexpr int kSubs = kStageK / GROUP;
-        __nv_bfloat162 off[kSubs];
-#pragma unroll
-        for (int g = 0; g < kSubs; ++g) {
-            uint32_t z = 8;
-            if (a.zero) z = __ldg(a.zero + v * a.G + min(kb * kSubs + g, a.G - 1)) & 15u;
-            const uint32_t o = 0x43004300u | (z * 0x00010001u);
-            off[g] = *reinterpret_cast<const __nv_bfloat162 *>(&o);
+        for (int i = 0; i < kRing - 1; ++i) {
+            if (f_kb < a.nkb) copy();
+            cp_async_commit();
         }
-        const int ab = s % kASlots;
-        if (!warp_wait(&bar.aempty[ab], ((s / kASlots) & 1) ^ 1)) return false;
-        tc_fence_after();
-        const uint32_t dst = tmem + kACol + ab * 64 + (static_cast<uint32_t>(quarter * 32) << 16);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (2 * h >= pieces) break;
-            uint32_t r[32];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int pc = 2 * h + j;
-                uint4 u = make_uint4(0, 0, 0, 0);
-                if (pc < pieces) u = *reinterpret_cast<const uint4 *>(row + ((pc ^ ((lane >> 1) & 3)) * 16));
-                const __nv_bfloat162 o = off[pc * 32 / GROUP];
-                widen8(u.x, o, r + j * 16);
-                widen8(u.y, o, r + j * 16 + 4);
-                widen8(u.z, o, r + j * 16 + 8);
-                widen8(u.w, o, r + j * 16 + 12);
+    }
+    __device__ bool run(const TokenPlan &t, int jobs, HeadBars &bar, const ParChunk *par, uint32_t tmem) {
+        const int stages = jobs * a.nkb;
+        int to_fetch = (stages - wi + Cfg::WW - 1) / Cfg::WW;
+        int kb = wi, c0 = 0;              // stage of the job; chunks of the jobs before it
+        const int chunks = (a.G + kParGroups - 1) / kParGroups;
+        int have = -1;                    // chunk of the parameter ring at hand
+        // start() left kRing - 1 groups, some perhaps empty: fill up in order.
+        int n = 0;                        // stages of this warpgroup done
+        auto fetch = [&]() {
+            if (f_n < to_fetch) {
+                while (f_kb >= a.nkb) {
+                    f_kb -= a.nkb;
+                    if (++f_pass == t.passes) { f_pass = 0; f_tile += gridDim.x; aim(); }
+                }
+                copy();
             }
-            tmem_st32(dst + h * 32, r);
+            cp_async_commit();
+        };
+        // Where the first tile had too few stages for the ring, restart the
+        // count: later groups complete later, so waiting by count stays right.
+        const int lead = f_n;             // stages in flight (<= kRing - 1)
+        for (int i = lead; i < kRing - 1; ++i) fetch();
+        for (int s = wi; s < stages; s += Cfg::WW, ++n) {
+            cp_async_wait<kRing - 2>();
+            __syncwarp();                 // every lane's copies of the stage have landed
+            fetch();
+            while (kb >= a.nkb) { kb -= a.nkb; c0 += chunks; }
+            const char *row = mine + (n % kRing) * kStageBytes + lane * 64;
+            const int np = pieces(kb);
+            uint32_t off[kSubs];
+            if (a.zero) {
+#pragma unroll
+                for (int g = 0; g < kSubs; ++g) {
+                    const int gi = min(kb * kSubs + g, a.G - 1), c = c0 + gi / kParGroups;
+                    while (have < c) {    // hand back the chunks behind it, wait for the next
+                        if (have >= 0) {
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bar.pempty[have % kParSlots]);
+                        }
+                        ++have;
+                        if (!warp_wait(&bar.pfull[have % kParSlots], (have / kParSlots) & 1)) return false;
+                    }
+                    off[g] = par[c % kParSlots].off[gi % kParGroups][quarter * 32 + lane];
+                }
+            } else {
+#pragma unroll
+                for (int g = 0; g < kSubs; ++g) off[g] = zero_pair(8);
+            }
+            const int ab = s % kASlots;
+            if (!warp_wait(&bar.aempty[ab], ((s / kASlots) & 1) ^ 1)) return false;
+            tc_fence_after();
+            const uint32_t dst = tmem + kACol + ab * 64 + (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (2 * h >= np) break;
+                uint32_t r[32];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int pc = 2 * h + j;
+                    uint4 u = make_uint4(0, 0, 0, 0);
+                    if (pc < np) u = *reinterpret_cast<const uint4 *>(row + ((pc ^ ((lane >> 1) & 3)) * 16));
+                    const uint32_t o = off[pc * 32 / GROUP];
+                    widen8(u.x, o, r + j * 16);
+                    widen8(u.y, o, r + j * 16 + 4);
+                    widen8(u.z, o, r + j * 16 + 8);
+                    widen8(u.w, o, r + j * 16 + 12);
+                }
+                tmem_st32(dst + h * 32, r);
+            }
+            tc_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bar.afull[ab]);
+            kb += Cfg::WW;
         }
-        tc_wait_st();
-        tc_fence_before();
-        mbar_arrive(&bar.afull[ab]);
-        if (++kb == a.nkb) {
-            kb = 0;
-            if (++pass == passes) { pass = 0; tile += gridDim.x; }
+        // Chunks that this warpgroup had no stage in (or its last ones).
+        if (a.zero) {
+            const int all = jobs * chunks;
+            for (; have < all; ++have) {
+                if (have >= 0) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.pempty[have % kParSlots]);
+                }
+                if (have + 1 < all && !warp_wait(&bar.pfull[(have + 1) % kParSlots], ((have + 1) / kParSlots) & 1))
+                    return false;
+            }
+        }
+        return true;
+    }
+};
+
+// One warpgroup per half of the tokens; a thread owns one vocabulary row.
+template <int NH>
+__device__ bool accumulate_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars &bar,
+                                const ParChunk *par, uint32_t tmem, int h) {
+    using Cfg = HeadCfg<NH>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarter = warp & 3;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    int i = 0, c = 0;
+    for (int job = 0; job < jobs; ++job) {
+        const int tile = blockIdx.x + job / t.passes * gridDim.x, pass = job % t.passes;
+        const int v = tile * kTileV + quarter * 32 + lane;
+        float acc[NH];
+#pragma unroll
+        for (int n = 0; n < NH; ++n) acc[n] = 0.f;
+        for (int g0 = 0; g0 < a.G; g0 += kParGroups, ++c) {
+            const int slot = c % kParSlots, ng = min(kParGroups, a.G - g0);
+            if (!warp_wait(&bar.pfull[slot], (c / kParSlots) & 1)) return false;
+            for (int q = 0; q < ng; ++q, ++i) {
+                const float sc = par[slot].scale[q][quarter * 32 + lane];
+                const float2 ss = make_float2(sc, sc);
+                const int db = h * Cfg::DB + i % Cfg::DB;
+                if (!warp_wait(&bar.dfull[db], (i / Cfg::DB) & 1)) return false;
+                tc_fence_after();
+                const uint32_t src = lanes + db * NH;
+                // The next 16 columns are on their way while these are added.
+                float d[2][16];
+                tmem_ld16(src, d[0]);
+#pragma unroll
+                for (int k = 0; k < NH / 16; ++k) {
+                    if (16 * k < t.nh) {
+                        tc_wait_ld(d[k & 1]);
+                        if (k + 1 < NH / 16 && 16 * (k + 1) < t.nh) tmem_ld16(src + 16 * (k + 1), d[(k + 1) & 1]);
+#pragma unroll
+                        for (int n = 0; n < 16; n += 2) {
+                            float *y = acc + 16 * k + n;
+                            const float2 z = __ffma2_rn(make_float2(d[k & 1][n], d[k & 1][n + 1]), ss, make_float2(y[0], y[1]));
+                            y[0] = z.x;
+                            y[1] = z.y;
+                        }
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(&bar.dempty[db]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.pempty[slot]);
+        }
+        // One vocabulary row per lane: a warp writes 32 consecutive logits of each token.
+        const int t0 = pass * t.per + h * t.nh, live = min(t.nh, t.count - t0);
+#pragma unroll
+        for (int n0 = 0; n0 < NH; n0 += 8) {
+            if (n0 < live) {
+                int row[8];
+#pragma unroll
+                for (int n = 0; n < 8; ++n) row[n] = __ldg(a.rows + t0 + min(n0 + n, live - 1));
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    if (n0 + n < live && v < a.V) {
+                        const long long at = static_cast<long long>(row[n]) * a.V + v;
+                        if (a.out_f32) static_cast<float *>(a.out)[at] = acc[n0 + n];
+                        else static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(acc[n0 + n]);
+                    }
+                }
+            }
         }
     }
     return true;
 }
 
 template <int NH, int GROUP>
-__global__ void __launch_bounds__(kHeadThreads, 1) head_kernel(HeadArgs a) {
+__global__ void __launch_bounds__(HeadCfg<NH>::kThreads, 1) head_kernel(HeadArgs a) {
     using Cfg = HeadCfg<NH>;
-    constexpr int DB = Cfg::DB, XS = Cfg::XS, kSubs = kStageK / GROUP;
     extern __shared__ char dyn[];
     __shared__ HeadBars bar;
     char *xring = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~static_cast<uintptr_t>(1023));
-    char *cring = xring + XS * Cfg::kXBytes;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = tid >> 7;
-    if (tid == 0) {
-        for (int i = 0; i < XS; ++i) { mbar_init(&bar.xfull[i], 1); mbar_init(&bar.xempty[i], 1); }
-        for (int i = 0; i < kASlots; ++i) { mbar_init(&bar.afull[i], 128); mbar_init(&bar.aempty[i], 1); }
-        for (int i = 0; i < 4; ++i) { mbar_init(&bar.dfull[i], 1); mbar_init(&bar.dempty[i], 128); }
-        mbar_init(&bar.drain, 1);
-        fence_mbar_init();
-    }
+    char *cring = xring + Cfg::XS * Cfg::kXBytes;
+    ParChunk *par = reinterpret_cast<ParChunk *>(cring + Cfg::CS * kStageBytes);
+    const int tid = threadIdx.x, warp = warp_value(tid >> 5), lane = tid & 31, wg = warp >> 2;
+    // The codes of the first stages are asked for at once: the pack kernel
+    // let this grid launch after its own wait, so whatever ran before this
+    // call has finished.
+    Widen<NH, GROUP> widen(a, cring, wg >= 1 && wg <= Cfg::WW ? wg - 1 : 0);
+    if (wg >= 1 && wg <= Cfg::WW) widen.start();
     if (warp == 0) tmem_alloc(&bar.tmem, kTmemCols);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = bar.tmem;
+    if (warp == 1 && lane == 0) {
+        for (int i = 0; i < Cfg::XS; ++i) { mbar_init(&bar.xfull[i], 1); mbar_init(&bar.xempty[i], 1); }
+        for (int i = 0; i < kASlots; ++i) { mbar_init(&bar.afull[i], 128); mbar_init(&bar.aempty[i], 1); }
+        for (int i = 0; i < 2 * Cfg::DB; ++i) { mbar_init(&bar.dfull[i], 1); mbar_init(&bar.dempty[i], 128); }
+        mbar_init(&bar.drain, 1);
+    }
     griddep_wait();
     griddep_launch_dependents();
     const TokenPlan t = token_plan(__ldcg(a.count), a.nh_max);
+    if (warp == 1 && lane == 0) {
+        for (int i = 0; i < kParSlots; ++i) {
+            mbar_init(&bar.pfull[i], 64);
+            mbar_init(&bar.pempty[i], 4 * t.halves + (a.zero ? 4 * Cfg::WW : 0));
+        }
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = warp_value(bar.tmem);
     const int my_tiles = (a.tiles - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) /
                          static_cast<int>(gridDim.x);
     const int jobs = my_tiles * t.passes;
     bool ok = true;
-
     if (wg == 0) {
-        regs_less<56>();
-        if (warp == 0 && lane == 0) {
-            const uint32_t bytes = t.per * 256;
-            int s = 0;
-            for (int job = 0; ok && job < jobs; ++job) {
-                const char *src = a.image + static_cast<long long>(job % t.passes) * a.nkb * bytes;
-                for (int kb = 0; kb < a.nkb; ++kb, ++s) {
-                    const int slot = s % XS;
-                    if (!mbar_wait(&bar.xempty[slot], ((s / XS) & 1) ^ 1, kHeadWaitNs)) { ok = false; break; }
-                    mbar_arrive_expect_tx(&bar.xfull[slot], bytes);
-                    bulk_g2s(xring + slot * Cfg::kXBytes, src + static_cast<long long>(kb) * bytes, bytes,
-                             &bar.xfull[slot]);
-                }
-            }
-            // The copies in flight land before this CTA may leave.
-            for (int q = max(0, s - XS); q < s; ++q)
-                mbar_wait(&bar.xfull[q % XS], (q / XS) & 1, kHeadWaitNs);
-        } else if (warp == 1 && lane == 0) {
-            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((t.nh >> 3) << 17) | ((kTileV >> 4) << 24);
-            int s = 0, i = 0;             // stage, group (both count through all jobs)
-            for (int job = 0; ok && job < jobs; ++job) {
-                for (int kb = 0; ok && kb < a.nkb; ++kb, ++s) {
-                    const int ab = s % kASlots, slot = s % XS;
-                    if (!mbar_wait(&bar.afull[ab], (s / kASlots) & 1, kHeadWaitNs) ||
-                        !mbar_wait(&bar.xfull[slot], (s / XS) & 1, kHeadWaitNs)) { ok = false; break; }
-                    tc_fence_after();
-                    const int subs = min(kSubs, (a.H - kb * kStageK) / GROUP);
-                    const uint32_t xs = smem_u32(xring + slot * Cfg::kXBytes);
-                    const uint32_t acol = tmem + kACol + ab * 64;
-                    for (int g = 0; ok && g < subs; ++g, ++i) {
-                        for (int h = 0; h < t.halves; ++h) {
-                            const int db = h * DB + i % DB;
-                            if (!mbar_wait(&bar.dempty[db], ((i / DB) & 1) ^ 1, kHeadWaitNs)) { ok = false; break; }
-                            tc_fence_after();
-#pragma unroll
-                            for (int q = 0; q < GROUP / 16; ++q) {
-                                const int k16 = g * (GROUP / 16) + q;
-                                const uint32_t b = xs + (h * 2 + (k16 >> 2)) * t.nh * 128 + (k16 & 3) * 32;
-                                mma_ts(tmem + db * NH, acol + 8 * k16, smem_desc(b), idesc, q > 0);
-                            }
-                            mma_commit(&bar.dfull[db]);
-                        }
-                    }
-                    if (ok) {
-                        mma_commit(&bar.aempty[ab]);
-                        mma_commit(&bar.xempty[slot]);
-                    }
-                }
-            }
-            // Nothing of the matrix unit is in flight when tensor memory is freed.
-            mma_commit(&bar.drain);
-            mbar_wait(&bar.drain, 0, kHeadWaitNs);
+        regs_less<Cfg::kRegs0>();
+        if (warp == 0) {
+            if (lane == 0) ok = copy_role<NH>(a, t, jobs, bar, xring);
+        } else if (warp == 1) {
+            ok = mma_role<NH, GROUP>(a, t, jobs, bar, xring, tmem);
+        } else {
+            ok = param_role(a, t, jobs, bar, par);
         }
-    } else if (wg == 1) {
-        regs_less<96>();
-        ok = widen_role<GROUP>(a, bar, cring, tmem, t.passes);
+    } else if (wg <= Cfg::WW) {
+        regs_less<Cfg::kRegsW>();
+        ok = widen.run(t, jobs, bar, par, tmem);
         cp_async_wait<0>();
     } else {
-        regs_more<176>();
-        const int h = wg - 2, quarter = warp & 3;
-        if (h < t.halves) {
-            const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-            int i = 0;
-            for (int job = 0; ok && job < jobs; ++job) {
-                const int tile = blockIdx.x + job / t.passes * gridDim.x, pass = job % t.passes;
-                const int v = tile * kTileV + quarter * 32 + lane;
-                const long long srow = static_cast<long long>(min(v, a.V - 1)) * a.G;
-                float acc[NH];
-#pragma unroll
-                for (int n = 0; n < NH; ++n) acc[n] = 0.f;
-                float next = ld_scale(a, srow);
-                for (int g = 0; g < a.G; ++g, ++i) {
-                    const float sc = next;
-                    next = ld_scale(a, srow + min(g + 1, a.G - 1));
-                    const int db = h * DB + i % DB;
-                    if (!warp_wait(&bar.dfull[db], (i / DB) & 1)) { ok = false; break; }
-                    tc_fence_after();
-                    const float2 ss = make_float2(sc, sc);
-#pragma unroll
-                    for (int c = 0; c < NH; c += 16) {
-                        if (c < t.nh) {
-                            float d[16];
-                            tmem_ld16(lanes + db * NH + c, d);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int n = 0; n < 16; n += 2) {
-                                const float2 y = __ffma2_rn(make_float2(d[n], d[n + 1]), ss,
-                                                            make_float2(acc[c + n], acc[c + n + 1]));
-                                acc[c + n] = y.x;
-                                acc[c + n + 1] = y.y;
-                            }
-                        }
-                    }
-                    tc_fence_before();
-                    mbar_arrive(&bar.dempty[db]);
-                }
-                if (!ok) break;
-                // One vocabulary row per lane: a warp writes 32 consecutive logits of each token.
-                const int t0 = pass * t.per + h * t.nh;
-#pragma unroll
-                for (int n = 0; n < NH; ++n) {
-                    if (n < t.nh && t0 + n < t.count && v < a.V) {
-                        const long long at = static_cast<long long>(__ldg(a.rows + t0 + n)) * a.V + v;
-                        if (a.out_f32) static_cast<float *>(a.out)[at] = acc[n];
-                        else static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(acc[n]);
-                    }
-                }
-            }
-        }
+        regs_more<Cfg::kRegsA>();
+        const int h = wg - 1 - Cfg::WW;
+        if (h < t.halves) ok = accumulate_role<NH>(a, t, jobs, bar, par, tmem, h);
     }
     if (!ok && a.status) atomicOr(a.status, SV_NOTE_TIMEOUT);
     __syncwarp();
@@ -557,7 +767,7 @@ static cudaError_t launch_head(const HeadArgs &a, cudaStream_t st) {
         if (e == cudaSuccess) attr_set[dev & 63].store(true, std::memory_order_release);
     }
     if (e != cudaSuccess) return e;
-    return launch_pdl(head_kernel<NH, GROUP>, dim3(a.tiles < sms ? a.tiles : sms), dim3(kHeadThreads),
+    return launch_pdl(head_kernel<NH, GROUP>, dim3(a.tiles < sms ? a.tiles : sms), dim3(HeadCfg<NH>::kThreads),
                       HeadCfg<NH>::kSmem, st, a);
 }
 
