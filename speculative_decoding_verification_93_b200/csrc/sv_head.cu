@@ -13,17 +13,17 @@
 //
 // One launch packs the scheduled tokens of x into the operand layout
 // (pack_kernel); the second (head_kernel) is persistent, one CTA per SM, and
-// walks 128-row tiles of the vocabulary, K in stages of 128:
-//   warp 0      copies the stage's x image into a ring of shared memory
-//               (bulk copies, mbarrier completion);
-//   warps 2, 3  fetch scales and zero points into a ring of their own;
-//   one or two warpgroups own one weight row per thread: codes arrive
-//               through a ring of asynchronous 16-byte copies, are widened to
-//               bf16 integers and written to tensor memory as the A operand;
+// walks 128-row tiles of the vocabulary, K in stages of AK (256, or 128 above
+// 128 tokens):
+//   warp 0      asks for each stage's codes (one TMA tile, swizzled);
+//   warp 2      copies each stage's x image (bulk copies);
+//   warp 3      fetches scales and zero points into a ring of their own;
 //   warp 1      issues tcgen05.mma, A from tensor memory, B from shared
-//               memory, one batch per (group, half of the tokens);
-//   two warpgroups, one per half of the tokens, read each finished batch
-//               back, scale and accumulate it, and write the logits.
+//               memory, one batch per (groups, half of the tokens);
+//   one or two warpgroups own one weight row per thread: they widen codes to
+//               bf16 integers and write them to tensor memory as A;
+//   one or two warpgroups, one per half of the tokens, read each finished
+//               batch back, scale and accumulate it, and write the logits.
 // The two halves alternate, so the matrix unit works on one half while the
 // other is read back.  A in tensor memory keeps the widened weights (four
 // times the bytes of the codes) out of shared memory, whose bandwidth the B
@@ -31,6 +31,7 @@
 #include <atomic>
 #include <climits>
 #include <cstdint>
+#include <cuda.h>
 
 #include "sv.h"
 #include "sv_device.cuh"
@@ -41,20 +42,21 @@ namespace sv {
 // ---------------------------------------------------------------------------
 // Layout shared by both kernels.
 // ---------------------------------------------------------------------------
-constexpr int kStageK = 128;             // k per stage
 constexpr int kTileV = 128;              // vocabulary rows per tile
 
 // Tokens are taken in `passes` of `per` tokens, each pass in `halves` of `nh`
 // (a multiple of 16) tokens.  The x image of (pass, stage) holds, per half,
-// two blocks of nh rows x 64 k in the 128-byte swizzle.
+// blocks of nh rows x 64 k in the 128-byte swizzle.
 struct TokenPlan {
     int count, passes, per, halves, nh;
 };
 
+// nh_max 16 takes at most 16 tokens, in one half.
 __host__ __device__ __forceinline__ TokenPlan token_plan(int count, int nh_max) {
     TokenPlan p;
     p.count = count;
-    p.passes = (count + 2 * nh_max - 1) / (2 * nh_max);
+    const int most = nh_max == 16 ? 16 : 2 * nh_max;
+    p.passes = (count + most - 1) / most;
     const int share = p.passes ? (count + p.passes - 1) / p.passes : 0;
     p.halves = share <= 16 ? 1 : 2;
     p.nh = p.halves == 1 ? 16 : (share + 31) / 32 * 16;
@@ -67,7 +69,8 @@ struct HeadArgs {
     const void *scale;
     const uint8_t *zero;
     bool scale_f32, out_f32;
-    int V, H, group, G, nkb, tiles;
+    int V, H, group, G, tiles;
+    int ak, nkb;         // k per stage, stages of a row
     const __nv_bfloat16 *x;
     int B, P;
     const int32_t *lengths;
@@ -152,9 +155,9 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(HeadArgs a) {
         w.y = __byte_perm(u.x, u.z, 0x7632);
         w.z = __byte_perm(u.y, u.w, 0x5410);
         w.w = __byte_perm(u.y, u.w, 0x7632);
-        const int kb = c / 16, sub = (c / 8) & 1, col = c & 7;
-        char *d = a.image + (static_cast<long long>(pass) * a.nkb + kb) * t.per * 256 +
-                  (half * 2 + sub) * t.nh * 128 + r * 128 + ((col ^ (r & 7)) * 16);
+        const int per_stage = a.ak / 8, kb = c / per_stage, sub = (c % per_stage) / 8, col = c & 7;
+        char *d = a.image + (static_cast<long long>(pass) * a.nkb + kb) * t.per * a.ak * 2 +
+                  (half * (a.ak / 64) + sub) * t.nh * 128 + r * 128 + ((col ^ (r & 7)) * 16);
         *reinterpret_cast<uint4 *>(d) = w;
     }
 }
@@ -220,12 +223,11 @@ template <int N> __device__ __forceinline__ void regs_more() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// One tile of a two-dimensional tensor map into shared memory.
+__device__ __forceinline__ void tma_tile(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
 }
 
 // Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups
@@ -238,12 +240,10 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
 // ---------------------------------------------------------------------------
 // 3. The product.
 // ---------------------------------------------------------------------------
-constexpr int kStageBytes = kTileV * kStageK / 2;   // codes of one stage
-constexpr int kASlots = 4;               // A operands in tensor memory: 64 columns each
-constexpr int kACol = 256;               // behind the accumulators
 constexpr uint32_t kTmemCols = 512;
 constexpr int kParGroups = 8;            // groups per chunk of the parameter ring
 constexpr int kParSlots = 3;
+constexpr int kDone = 8;                 // ring of stage-done barriers
 constexpr uint64_t kHeadWaitNs = 1000000000ull;
 
 // Scale and zero point of kParGroups groups of a tile's rows.  `off` is the
@@ -253,36 +253,53 @@ struct ParChunk {
     uint32_t off[kParGroups][kTileV];
 };
 
-// Per instantiation: up to NH tokens a half, DB accumulators per half, XS
-// stages of x, CS stages of codes, WW warpgroups that widen codes.
-// One warpgroup widens a stage in about 400 cycles (latency; 200 of issue),
-// the copies of a stage's codes take 350, and the matrix unit 8 nh cycles:
-// above 64 tokens a half one is enough, and the accumulators need the
-// registers of the second.
-template <int NH> struct HeadCfg {
-    static constexpr int DB = NH <= 16 ? 4 : NH <= 64 ? 2 : 1;
-    static constexpr int XS = NH <= 16 ? 8 : NH <= 64 ? 3 : 2;
-    static constexpr int CS = NH <= 64 ? 12 : 8;
+// Up to NH tokens a half, for weights in groups of GROUP.  AK k per stage, AS
+// A operands in tensor memory (AK / 2 columns each, behind the accumulators),
+// CS and XS stages of codes and x in shared memory, WW warpgroups that widen,
+// AW that accumulate.  A batch is GB groups of one half; DB batches of a half
+// are in tensor memory at a time.
+//   NH = 16: waiting is all that costs, so a batch is a whole stage.
+//   NH = 64: a stage of 256 k, whose widening two warpgroups share.
+//   NH = 96: the matrix unit sets the pace (8 nh cycles for 128 k; one
+//   warpgroup widens that in about 450), and needs two batches a half so that
+//   it never waits for the read-back: 384 columns, which leaves A two stages
+//   of 128 k.
+template <int NH, int GROUP> struct HeadCfg {
+    static constexpr int AK = NH <= 64 ? 256 : 128;
+    static constexpr int AS = 2;
     static constexpr int WW = NH <= 64 ? 2 : 1;
-    static constexpr int kThreads = 128 * (3 + WW);
+    static constexpr int AW = NH <= 16 ? 1 : 2;
+    static constexpr int GB = NH <= 16 ? AK / GROUP : 1;
+    static constexpr int DB = NH <= 16 ? (GROUP == 32 ? 2 : 4) : 2;
+    static constexpr int XS = NH <= 16 ? 4 : NH <= 64 ? 2 : 3;
+    static constexpr int CS = NH <= 16 ? 8 : NH <= 64 ? 4 : 5;
+    static constexpr int kSubs = AK / GROUP;
+    static constexpr int kACol = AW * DB * GB * NH;
+    static constexpr int kThreads = 128 * (1 + WW + AW);
     // Registers a thread of the service, widening and accumulating
-    // warpgroups: their sum stays below what the CTA was launched with.
-    static constexpr int kRegs0 = 56, kRegsW = WW == 2 ? 80 : 88, kRegsA = WW == 2 ? 128 : 184;
+    // warpgroups: their sum stays within what the CTA was launched with.
+    static constexpr int kRegs0 = 72;
+    static constexpr int kRegsW = NH <= 16 ? 96 : NH <= 64 ? 80 : 72;
+    static constexpr int kRegsA = NH <= 16 ? 136 : NH <= 64 ? 120 : 184;
     static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
-    static_assert(kRegs0 + WW * kRegsW + 2 * kRegsA <= (3 + WW) * kLaunchRegs, "register split");
-    static constexpr int kXBytes = 2 * NH * 256;
+    static_assert(kRegs0 + WW * kRegsW + AW * kRegsA <= (1 + WW + AW) * kLaunchRegs, "register split");
+    static constexpr int kCodeBytes = kTileV * AK / 2;
+    static constexpr int kXBytes = AW * NH * AK * 2;
     // At least half of the SM's shared memory: two CTAs on one SM would
     // wait for each other's tensor memory.
-    static constexpr int kUsed = 1024 + XS * kXBytes + CS * kStageBytes +
+    static constexpr int kUsed = 1024 + XS * kXBytes + CS * kCodeBytes +
                                  kParSlots * static_cast<int>(sizeof(ParChunk));
     static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
-    static_assert(CS % WW == 0 && 2 * NH * DB <= kACol && kSmem <= 227 * 1024 - 1024, "head layout");
+    static_assert(kSmem <= 227 * 1024 - 1024 && kACol + AS * AK / 2 <= static_cast<int>(kTmemCols), "head layout");
+    static_assert(XS < kDone && AS < kDone && 2 + AW <= 32 && kParGroups % GB == 0, "head rings");
 };
 
 struct HeadBars {
-    uint64_t xfull[8], xempty[8];
-    uint64_t afull[kASlots], aempty[kASlots];
-    uint64_t dfull[8], dempty[8];
+    uint64_t cfull[8], cempty[8];        // codes landed; read by the widening warps
+    uint64_t xfull[4];                   // x landed
+    uint64_t afull[2];                   // A written
+    uint64_t done[kDone];                // the matrix unit is through a stage: its x and A are free
+    uint64_t dfull[8], dempty[8];        // a batch finished; read back
     uint64_t pfull[kParSlots], pempty[kParSlots];
     uint64_t drain;
     uint32_t tmem;
@@ -321,75 +338,113 @@ __device__ __forceinline__ uint32_t zero_pair(uint32_t z) {
     return *reinterpret_cast<const uint32_t *>(&p);
 }
 
-// The x images of every stage into shared memory (one lane of warp 0).
-template <int NH>
-__device__ bool copy_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars &bar, char *xring) {
-    using Cfg = HeadCfg<NH>;
-    const uint32_t bytes = t.per * 256;
+// Codes of every stage (one lane).  start() asks for the first tile's before
+// the token count is known.
+template <typename Cfg> struct CodeCopy {
+    const HeadArgs &a;
+    const CUtensorMap *map;
+    HeadBars &bar;
+    char *ring;
+    int s = 0;
+    __device__ CodeCopy(const HeadArgs &a_, const CUtensorMap *m, HeadBars &b, char *r) : a(a_), map(m), bar(b), ring(r) {}
+    __device__ __forceinline__ void copy(int tile, int kb) {
+        const int slot = s % Cfg::CS;
+        mbar_arrive_expect_tx(&bar.cfull[slot], Cfg::kCodeBytes);
+        tma_tile(ring + slot * Cfg::kCodeBytes, map, kb * (Cfg::AK / 2), tile * kTileV, &bar.cfull[slot]);
+        ++s;
+    }
+    __device__ void start() {
+        for (int kb = 0; kb < min(a.nkb, Cfg::CS); ++kb) copy(blockIdx.x, kb);
+    }
+    __device__ bool run(const TokenPlan &t, int jobs) {
+        bool ok = true;
+        int q = 0;
+        for (int job = 0; ok && job < jobs; ++job) {
+            const int tile = blockIdx.x + job / t.passes * gridDim.x;
+            for (int kb = 0; kb < a.nkb; ++kb, ++q) {
+                if (q < s) continue;      // asked for by start()
+                if (!mbar_wait(&bar.cempty[s % Cfg::CS], ((s / Cfg::CS) & 1) ^ 1, kHeadWaitNs)) { ok = false; break; }
+                copy(tile, kb);
+            }
+        }
+        // The copies in flight land before this CTA may leave.
+        for (int i = max(0, s - Cfg::CS); i < s; ++i)
+            mbar_wait(&bar.cfull[i % Cfg::CS], (i / Cfg::CS) & 1, kHeadWaitNs);
+        return ok;
+    }
+};
+
+// The x images of every stage (one lane).
+template <typename Cfg>
+__device__ bool x_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars &bar, char *xring) {
+    const uint32_t bytes = t.per * Cfg::AK * 2;
     bool ok = true;
     int s = 0;
     for (int job = 0; ok && job < jobs; ++job) {
         const char *src = a.image + static_cast<long long>(job % t.passes) * a.nkb * bytes;
         for (int kb = 0; kb < a.nkb; ++kb, ++s) {
-            const int slot = s % Cfg::XS;
-            if (!mbar_wait(&bar.xempty[slot], ((s / Cfg::XS) & 1) ^ 1, kHeadWaitNs)) { ok = false; break; }
+            const int slot = s % Cfg::XS, old = s - Cfg::XS;
+            if (old >= 0 && !mbar_wait(&bar.done[old % kDone], (old / kDone) & 1, kHeadWaitNs)) { ok = false; break; }
             mbar_arrive_expect_tx(&bar.xfull[slot], bytes);
             bulk_g2s(xring + slot * Cfg::kXBytes, src + static_cast<long long>(kb) * bytes, bytes, &bar.xfull[slot]);
         }
     }
-    // The copies in flight land before this CTA may leave.
     for (int q = max(0, s - Cfg::XS); q < s; ++q)
         mbar_wait(&bar.xfull[q % Cfg::XS], (q / Cfg::XS) & 1, kHeadWaitNs);
     return ok;
 }
 
 // The matrix unit's instructions (warp 1: every lane runs the loops, so that
-// the operands stay in uniform registers; one lane issues).
-template <int NH, int GROUP>
+// the operands stay in uniform registers; one lane issues).  What a batch
+// waits for is waited for at once, one barrier a lane: each wait costs some
+// 80 cycles even when nothing is missing, more than the eight instructions
+// of a batch.
+template <typename Cfg, int NH, int GROUP>
 __device__ bool mma_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars &bar, const char *xring,
                          uint32_t tmem) {
-    using Cfg = HeadCfg<NH>;
-    constexpr int kSubs = kStageK / GROUP;
+    constexpr int kBatches = Cfg::kSubs / Cfg::GB;   // of one half in a stage
+    const int lane = threadIdx.x & 31;
     const uint32_t nh = warp_value(t.nh);
     const int halves = warp_value(t.halves), stages = warp_value(jobs) * a.nkb;
     const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((nh >> 3) << 17) | ((kTileV >> 4) << 24);
     const uint64_t x0 = smem_desc(smem_u32(xring));
     const bool issuer = elect_one();
-    int i = 0, kb = 0;                    // group (counts through all jobs), stage of the job
+    int i = 0, kb = 0;                    // batch of a half (counts through all jobs), stage of the job
     bool ok = true;
     for (int s = 0; s < stages; ++s) {
-        const int ab = s % kASlots, slot = s % Cfg::XS;
-        if (!warp_wait(&bar.afull[ab], (s / kASlots) & 1) ||
-            !warp_wait(&bar.xfull[slot], (s / Cfg::XS) & 1)) { ok = false; break; }
-        const int subs = min(kSubs, (a.H - kb * kStageK) / GROUP);
+        const int ab = s % Cfg::AS, slot = s % Cfg::XS;
+        const int subs = min(Cfg::kSubs, (a.H - kb * Cfg::AK) / GROUP);
         const uint64_t xs = x0 + static_cast<uint64_t>(slot * (Cfg::kXBytes / 16));
-        const uint32_t acol = tmem + kACol + ab * 64;
+        const uint32_t acol = tmem + Cfg::kACol + ab * (Cfg::AK / 2);
 #pragma unroll
-        for (int g = 0; g < kSubs; ++g) {
-            if (g >= subs) break;
-            for (int h = 0; h < halves; ++h) {
-                const int db = h * Cfg::DB + i % Cfg::DB;
-                if (!warp_wait(&bar.dempty[db], ((i / Cfg::DB) & 1) ^ 1)) { ok = false; break; }
-                tc_fence_after();
-                if (issuer) {
-                    const uint64_t xh = xs + static_cast<uint64_t>(h * 2 * nh * 8);
+        for (int j = 0; j < kBatches; ++j) {
+            if (j * Cfg::GB >= subs) break;
+            const int d = i % Cfg::DB;
+            uint64_t *b = &bar.dempty[(lane & 1 ? halves - 1 : 0) * Cfg::DB + d];
+            uint32_t parity = ((i / Cfg::DB) & 1) ^ 1;
+            if (j == 0 && lane == 2) { b = &bar.afull[ab]; parity = (s / Cfg::AS) & 1; }
+            if (j == 0 && lane == 3) { b = &bar.xfull[slot]; parity = (s / Cfg::XS) & 1; }
+            if (!warp_wait(b, parity)) { ok = false; break; }
+            tc_fence_after();
+            if (issuer) {
+                for (int h = 0; h < halves; ++h) {
+                    const int db = h * Cfg::DB + d;
+                    const uint64_t xh = xs + static_cast<uint64_t>(h * (Cfg::AK / 64) * nh * 8);
 #pragma unroll
-                    for (int q = 0; q < GROUP / 16; ++q) {
-                        const int k16 = g * (GROUP / 16) + q;
-                        mma_ts(tmem + db * NH, acol + 8 * k16, xh + (k16 >> 2) * nh * 8 + (k16 & 3) * 2, idesc, q > 0);
+                    for (int q = 0; q < Cfg::GB * GROUP / 16; ++q) {
+                        const int k16 = j * (Cfg::GB * GROUP / 16) + q, g = q / (GROUP / 16);
+                        if (Cfg::GB > 1 && j * Cfg::GB + g >= subs) break;
+                        mma_ts(tmem + (db * Cfg::GB + g) * NH, acol + 8 * k16,
+                               xh + (k16 >> 2) * nh * 8 + (k16 & 3) * 2, idesc, q % (GROUP / 16) > 0);
                     }
                     mma_commit(&bar.dfull[db]);
                 }
-                __syncwarp();
             }
-            if (!ok) break;
+            __syncwarp();
             ++i;
         }
         if (!ok) break;
-        if (issuer) {
-            mma_commit(&bar.aempty[ab]);
-            mma_commit(&bar.xempty[slot]);
-        }
+        if (issuer) mma_commit(&bar.done[s % kDone]);
         __syncwarp();
         if (++kb == a.nkb) kb = 0;
     }
@@ -400,232 +455,183 @@ __device__ bool mma_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBa
     return ok;
 }
 
-// Scales and zero points (warps 2 and 3, two rows a lane): as fp32 and bf16
-// pairs in shared memory, eight groups at a time, so that the rows' strided
-// reads are 16 bytes wide where the alignment allows it, made once for both
-// halves, and far ahead of their use.
+// Scales and zero points (warp 3, four rows a lane): as fp32 and bf16 pairs
+// in shared memory, eight groups at a time, so that the rows' strided reads
+// are 16 and 8 bytes wide where the alignment allows it, made once for both
+// halves, and ahead of their use.
 __device__ bool param_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars &bar, ParChunk *ring) {
-    const int l = threadIdx.x & 63;       // warps 2 and 3
-    const bool wide = !a.scale_f32 && a.G % 8 == 0 && (reinterpret_cast<uintptr_t>(a.scale) & 15) == 0;
+    constexpr int kRows = kTileV / 32;
+    const int lane = threadIdx.x & 31;
+    const bool wide = !a.scale_f32 && a.G % 8 == 0 && (reinterpret_cast<uintptr_t>(a.scale) & 15) == 0 &&
+                      (reinterpret_cast<uintptr_t>(a.zero) & 7) == 0;
     int c = 0;
     for (int job = 0; job < jobs; ++job) {
         const int tile = blockIdx.x + job / t.passes * gridDim.x;
         for (int g0 = 0; g0 < a.G; g0 += kParGroups, ++c) {
-            float sc[2][kParGroups];
-            uint32_t zp[2][kParGroups];
+            ParChunk &p = ring[c % kParSlots];
+            long long at[kRows];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const long long at = static_cast<long long>(min(tile * kTileV + r * 64 + l, a.V - 1)) * a.G + g0;
-                if (wide) {
-                    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.scale) + at));
-                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+            for (int r = 0; r < kRows; ++r)
+                at[r] = static_cast<long long>(min(tile * kTileV + r * 32 + lane, a.V - 1)) * a.G + g0;
+            if (wide) {
+                uint4 u[kRows];
+                uint2 z[kRows];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) { sc[r][2 * q] = bf16_lo(w[q]); sc[r][2 * q + 1] = bf16_hi(w[q]); }
-                } else {
+                for (int r = 0; r < kRows; ++r) {
+                    u[r] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.scale) + at[r]));
+                    z[r] = a.zero ? __ldg(reinterpret_cast<const uint2 *>(a.zero + at[r])) : make_uint2(0, 0);
+                }
+                if (!warp_wait(&bar.pempty[c % kParSlots], ((c / kParSlots) & 1) ^ 1)) return false;
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    const uint32_t w[4] = {u[r].x, u[r].y, u[r].z, u[r].w};
 #pragma unroll
                     for (int q = 0; q < kParGroups; ++q) {
-                        const long long e = at + min(q, a.G - 1 - g0);
-                        sc[r][q] = a.scale_f32 ? __ldg(static_cast<const float *>(a.scale) + e)
-                                               : ld_elem<2>(static_cast<const char *>(a.scale), e);
+                        p.scale[q][r * 32 + lane] = 64.f * (q & 1 ? bf16_hi(w[q / 2]) : bf16_lo(w[q / 2]));
+                        if (a.zero)
+                            p.off[q][r * 32 + lane] = zero_pair((q < 4 ? z[r].x : z[r].y) >> (8 * (q & 3)) & 15u);
                     }
                 }
-                if (a.zero) {
+            } else {
+                if (!warp_wait(&bar.pempty[c % kParSlots], ((c / kParSlots) & 1) ^ 1)) return false;
 #pragma unroll
-                    for (int q = 0; q < kParGroups; ++q) zp[r][q] = __ldg(a.zero + at + min(q, a.G - 1 - g0)) & 15u;
+                for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+                    for (int q = 0; q < kParGroups; ++q) {
+                        const long long e = at[r] + min(q, a.G - 1 - g0);
+                        p.scale[q][r * 32 + lane] =
+                            64.f * (a.scale_f32 ? __ldg(static_cast<const float *>(a.scale) + e)
+                                                : ld_elem<2>(static_cast<const char *>(a.scale), e));
+                        if (a.zero) p.off[q][r * 32 + lane] = zero_pair(__ldg(a.zero + e) & 15u);
+                    }
                 }
             }
-            ParChunk &p = ring[c % kParSlots];
-            if (!warp_wait(&bar.pempty[c % kParSlots], ((c / kParSlots) & 1) ^ 1)) return false;
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int q = 0; q < kParGroups; ++q) {
-                    p.scale[q][r * 64 + l] = 64.f * sc[r][q];
-                    if (a.zero) p.off[q][r * 64 + l] = zero_pair(zp[r][q]);
-                }
             mbar_arrive(&bar.pfull[c % kParSlots]);
         }
     }
     return true;
 }
 
-// One warpgroup of wi = 0 .. WW - 1: the stages s = wi mod WW, one weight row a
-// thread.  Codes come by asynchronous 16-byte copies, four lanes a row (64
-// contiguous bytes), each warp for its own 32 rows.
-template <int NH, int GROUP> struct Widen {
-    using Cfg = HeadCfg<NH>;
-    static constexpr int kRing = Cfg::CS / Cfg::WW;   // slots of this warpgroup
-    static constexpr int kSubs = kStageK / GROUP;
-    const HeadArgs &a;
-    char *mine;                           // this warp's rows of the warpgroup's first slot
-    int lane, quarter, wi;
-    int f_kb, f_pass, f_tile, f_n;        // next stage to fetch, stages fetched
-    const uint8_t *src[4];                // this lane's rows in the tile being fetched
-
-    __device__ Widen(const HeadArgs &args, char *ring, int wi_) : a(args), wi(wi_) {
-        lane = threadIdx.x & 31;
-        quarter = (threadIdx.x >> 5) & 3;
-        mine = ring + wi * kRing * kStageBytes + quarter * 32 * 64;
-        f_kb = wi; f_pass = 0; f_tile = blockIdx.x; f_n = 0;
-        aim();
-    }
-    __device__ __forceinline__ void aim() {
+// One of WW warpgroups: its share of every stage's k (128), one weight row a
+// thread.
+template <typename Cfg, int GROUP>
+__device__ bool widen_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars &bar, const char *ring,
+                           const ParChunk *par, uint32_t tmem, int wi) {
+    constexpr int kRowBytes = Cfg::AK / 2, kMine = 128 / GROUP;   // groups of this share
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
+    const int stages = jobs * a.nkb, chunks = (a.G + kParGroups - 1) / kParGroups;
+    const int r = quarter * 32 + lane;
+    // The copy's swizzle: 16-byte pieces of 128-byte (64-byte) rows.
+    const int swz = kRowBytes == 128 ? r & 7 : (r >> 1) & 3;
+    const uint32_t dst0 = tmem + Cfg::kACol + wi * 64 + (static_cast<uint32_t>(quarter * 32) << 16);
+    int kb = 0, c0 = 0, have = -1;        // stage of the job, chunks before the job, chunk at hand
+    uint32_t off[kMine];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const long long v = min(f_tile * kTileV + quarter * 32 + 8 * i + (lane >> 2), a.V - 1);
-            src[i] = a.codes + v * (a.H / 2) + (lane & 3) * 16;
+    for (int g = 0; g < kMine; ++g) off[g] = zero_pair(8);
+    // Hand back chunk `have`, wait for the next one.
+    auto next_chunk = [&](bool wait) {
+        if (have >= 0) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.pempty[have % kParSlots]);
         }
-    }
-    // 32-code pieces of stage kb.
-    __device__ __forceinline__ int pieces(int kb) const { return min(4, a.H / 32 - 4 * kb); }
-    __device__ __forceinline__ void copy() {
-        char *slot = mine + (f_n % kRing) * kStageBytes;
-        if ((lane & 3) < pieces(f_kb)) {
+        ++have;
+        return !wait || warp_wait(&bar.pfull[have % kParSlots], (have / kParSlots) & 1);
+    };
+    for (int s = 0; s < stages; ++s) {
+        const int slot = s % Cfg::CS, ab = s % Cfg::AS, old = s - Cfg::AS;
+        if (!warp_wait(&bar.cfull[slot], (s / Cfg::CS) & 1)) return false;
+        const char *row = ring + slot * Cfg::kCodeBytes + r * kRowBytes;
+        uint4 u[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 8 * i + (lane >> 2);
-                cp_async16(slot + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) * 16), src[i] + f_kb * 64);
-            }
-        }
-        ++f_n;
-        f_kb += Cfg::WW;
-    }
-    // The first stages of the first tile, whatever the token count.
-    __device__ void start() {
-#pragma unroll 1
-        for (int i = 0; i < kRing - 1; ++i) {
-            if (f_kb < a.nkb) copy();
-            cp_async_commit();
-        }
-    }
-    __device__ bool run(const TokenPlan &t, int jobs, HeadBars &bar, const ParChunk *par, uint32_t tmem) {
-        const int stages = jobs * a.nkb;
-        int to_fetch = (stages - wi + Cfg::WW - 1) / Cfg::WW;
-        int kb = wi, c0 = 0;              // stage of the job; chunks of the jobs before it
-        const int chunks = (a.G + kParGroups - 1) / kParGroups;
-        int have = -1;                    // chunk of the parameter ring at hand
-        // start() left kRing - 1 groups, some perhaps empty: fill up in order.
-        int n = 0;                        // stages of this warpgroup done
-        auto fetch = [&]() {
-            if (f_n < to_fetch) {
-                while (f_kb >= a.nkb) {
-                    f_kb -= a.nkb;
-                    if (++f_pass == t.passes) { f_pass = 0; f_tile += gridDim.x; aim(); }
-                }
-                copy();
-            }
-            cp_async_commit();
-        };
-        // Where the first tile had too few stages for the ring, restart the
-        // count: later groups complete later, so waiting by count stays right.
-        const int lead = f_n;             // stages in flight (<= kRing - 1)
-        for (int i = lead; i < kRing - 1; ++i) fetch();
-        for (int s = wi; s < stages; s += Cfg::WW, ++n) {
-            cp_async_wait<kRing - 2>();
-            __syncwarp();                 // every lane's copies of the stage have landed
-            fetch();
-            while (kb >= a.nkb) { kb -= a.nkb; c0 += chunks; }
-            const char *row = mine + (n % kRing) * kStageBytes + lane * 64;
-            const int np = pieces(kb);
-            uint32_t off[kSubs];
-            if (a.zero) {
-#pragma unroll
-                for (int g = 0; g < kSubs; ++g) {
-                    const int gi = min(kb * kSubs + g, a.G - 1), c = c0 + gi / kParGroups;
-                    while (have < c) {    // hand back the chunks behind it, wait for the next
-                        if (have >= 0) {
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&bar.pempty[have % kParSlots]);
-                        }
-                        ++have;
-                        if (!warp_wait(&bar.pfull[have % kParSlots], (have / kParSlots) & 1)) return false;
-                    }
-                    off[g] = par[c % kParSlots].off[gi % kParGroups][quarter * 32 + lane];
-                }
-            } else {
-#pragma unroll
-                for (int g = 0; g < kSubs; ++g) off[g] = zero_pair(8);
-            }
-            const int ab = s % kASlots;
-            if (!warp_wait(&bar.aempty[ab], ((s / kASlots) & 1) ^ 1)) return false;
-            tc_fence_after();
-            const uint32_t dst = tmem + kACol + ab * 64 + (static_cast<uint32_t>(quarter * 32) << 16);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (2 * h >= np) break;
-                uint32_t r[32];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int pc = 2 * h + j;
-                    uint4 u = make_uint4(0, 0, 0, 0);
-                    if (pc < np) u = *reinterpret_cast<const uint4 *>(row + ((pc ^ ((lane >> 1) & 3)) * 16));
-                    const uint32_t o = off[pc * 32 / GROUP];
-                    widen8(u.x, o, r + j * 16);
-                    widen8(u.y, o, r + j * 16 + 4);
-                    widen8(u.z, o, r + j * 16 + 8);
-                    widen8(u.w, o, r + j * 16 + 12);
-                }
-                tmem_st32(dst + h * 32, r);
-            }
-            tc_wait_st();
-            tc_fence_before();
-            mbar_arrive(&bar.afull[ab]);
-            kb += Cfg::WW;
-        }
-        // Chunks that this warpgroup had no stage in (or its last ones).
+        for (int j = 0; j < 4; ++j) u[j] = *reinterpret_cast<const uint4 *>(row + (((4 * wi + j) ^ swz) * 16));
         if (a.zero) {
-            const int all = jobs * chunks;
-            for (; have < all; ++have) {
-                if (have >= 0) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.pempty[have % kParSlots]);
-                }
-                if (have + 1 < all && !warp_wait(&bar.pfull[(have + 1) % kParSlots], ((have + 1) / kParSlots) & 1))
-                    return false;
+#pragma unroll
+            for (int g = 0; g < kMine; ++g) {
+                const int gi = min(kb * Cfg::kSubs + wi * kMine + g, a.G - 1), c = c0 + gi / kParGroups;
+                while (have < c)
+                    if (!next_chunk(true)) return false;
+                off[g] = par[c % kParSlots].off[gi % kParGroups][r];
             }
         }
-        return true;
+        if (old >= 0 && !warp_wait(&bar.done[old % kDone], (old / kDone) & 1)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t w[32];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint4 &v = u[2 * h + j];
+                const uint32_t o = off[(2 * h + j) * 32 / GROUP];
+                widen8(v.x, o, w + j * 16);
+                widen8(v.y, o, w + j * 16 + 4);
+                widen8(v.z, o, w + j * 16 + 8);
+                widen8(v.w, o, w + j * 16 + 12);
+            }
+            tmem_st32(dst0 + ab * (Cfg::AK / 2) + h * 32, w);
+        }
+        // The codes are in registers in every lane of this warp.
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.cempty[slot]);
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bar.afull[ab]);
+        if (++kb == a.nkb) { kb = 0; c0 += chunks; }
     }
-};
+    if (a.zero)
+        for (const int all = jobs * chunks; have < all;)
+            if (!next_chunk(have + 1 < all)) return false;
+    return true;
+}
 
 // One warpgroup per half of the tokens; a thread owns one vocabulary row.
-template <int NH>
+template <typename Cfg, int NH>
 __device__ bool accumulate_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars &bar,
                                 const ParChunk *par, uint32_t tmem, int h) {
-    using Cfg = HeadCfg<NH>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarter = warp & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     int i = 0, c = 0;
     for (int job = 0; job < jobs; ++job) {
         const int tile = blockIdx.x + job / t.passes * gridDim.x, pass = job % t.passes;
         const int v = tile * kTileV + quarter * 32 + lane;
+        // Output rows of this half's tokens, 32 to a register across the lanes.
+        const int t0 = pass * t.per + h * t.nh, live = min(t.nh, t.count - t0);
+        int rows[(NH + 31) / 32];
+#pragma unroll
+        for (int n = 0; n < (NH + 31) / 32; ++n)
+            rows[n] = 32 * n < live ? __ldg(a.rows + t0 + min(32 * n + lane, live - 1)) : 0;
         float acc[NH];
 #pragma unroll
         for (int n = 0; n < NH; ++n) acc[n] = 0.f;
         for (int g0 = 0; g0 < a.G; g0 += kParGroups, ++c) {
             const int slot = c % kParSlots, ng = min(kParGroups, a.G - g0);
             if (!warp_wait(&bar.pfull[slot], (c / kParSlots) & 1)) return false;
-            for (int q = 0; q < ng; ++q, ++i) {
-                const float sc = par[slot].scale[q][quarter * 32 + lane];
-                const float2 ss = make_float2(sc, sc);
+            for (int q0 = 0; q0 < ng; q0 += Cfg::GB, ++i) {
                 const int db = h * Cfg::DB + i % Cfg::DB;
                 if (!warp_wait(&bar.dfull[db], (i / Cfg::DB) & 1)) return false;
                 tc_fence_after();
-                const uint32_t src = lanes + db * NH;
-                // The next 16 columns are on their way while these are added.
-                float d[2][16];
-                tmem_ld16(src, d[0]);
 #pragma unroll
-                for (int k = 0; k < NH / 16; ++k) {
-                    if (16 * k < t.nh) {
-                        tc_wait_ld(d[k & 1]);
-                        if (k + 1 < NH / 16 && 16 * (k + 1) < t.nh) tmem_ld16(src + 16 * (k + 1), d[(k + 1) & 1]);
+                for (int q = 0; q < Cfg::GB; ++q) {
+                    if (Cfg::GB > 1 && q0 + q >= ng) break;
+                    const float sc = par[slot].scale[q0 + q][quarter * 32 + lane];
+                    const float2 ss = make_float2(sc, sc);
+                    const uint32_t src = lanes + (db * Cfg::GB + q) * NH;
+                    // The next 16 columns are on their way while these are added.
+                    float d[2][16];
+                    tmem_ld16(src, d[0]);
 #pragma unroll
-                        for (int n = 0; n < 16; n += 2) {
-                            float *y = acc + 16 * k + n;
-                            const float2 z = __ffma2_rn(make_float2(d[k & 1][n], d[k & 1][n + 1]), ss, make_float2(y[0], y[1]));
-                            y[0] = z.x;
-                            y[1] = z.y;
+                    for (int k = 0; k < NH / 16; ++k) {
+                        if (16 * k < t.nh) {
+                            tc_wait_ld(d[k & 1]);
+                            if (k + 1 < NH / 16 && 16 * (k + 1) < t.nh)
+                                tmem_ld16(src + 16 * (k + 1), d[(k + 1) & 1]);
+#pragma unroll
+                            for (int n = 0; n < 16; n += 2) {
+                                float *y = acc + 16 * k + n;
+                                const float2 z = __ffma2_rn(make_float2(d[k & 1][n], d[k & 1][n + 1]), ss,
+                                                            make_float2(y[0], y[1]));
+                                y[0] = z.x;
+                                y[1] = z.y;
+                            }
                         }
                     }
                 }
@@ -636,20 +642,13 @@ __device__ bool accumulate_role(const HeadArgs &a, const TokenPlan &t, int jobs,
             if (lane == 0) mbar_arrive(&bar.pempty[slot]);
         }
         // One vocabulary row per lane: a warp writes 32 consecutive logits of each token.
-        const int t0 = pass * t.per + h * t.nh, live = min(t.nh, t.count - t0);
 #pragma unroll
-        for (int n0 = 0; n0 < NH; n0 += 8) {
-            if (n0 < live) {
-                int row[8];
-#pragma unroll
-                for (int n = 0; n < 8; ++n) row[n] = __ldg(a.rows + t0 + min(n0 + n, live - 1));
-#pragma unroll
-                for (int n = 0; n < 8; ++n) {
-                    if (n0 + n < live && v < a.V) {
-                        const long long at = static_cast<long long>(row[n]) * a.V + v;
-                        if (a.out_f32) static_cast<float *>(a.out)[at] = acc[n0 + n];
-                        else static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(acc[n0 + n]);
-                    }
+        for (int n = 0; n < NH; ++n) {
+            if (n < live) {
+                const long long at = static_cast<long long>(__shfl_sync(0xffffffffu, rows[n / 32], n % 32)) * a.V + v;
+                if (v < a.V) {
+                    if (a.out_f32) static_cast<float *>(a.out)[at] = acc[n];
+                    else static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(acc[n]);
                 }
             }
         }
@@ -658,32 +657,36 @@ __device__ bool accumulate_role(const HeadArgs &a, const TokenPlan &t, int jobs,
 }
 
 template <int NH, int GROUP>
-__global__ void __launch_bounds__(HeadCfg<NH>::kThreads, 1) head_kernel(HeadArgs a) {
-    using Cfg = HeadCfg<NH>;
+__global__ void __launch_bounds__(HeadCfg<NH, GROUP>::kThreads, 1)
+head_kernel(HeadArgs a, const __grid_constant__ CUtensorMap map) {
+    using Cfg = HeadCfg<NH, GROUP>;
     extern __shared__ char dyn[];
     __shared__ HeadBars bar;
     char *xring = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~static_cast<uintptr_t>(1023));
     char *cring = xring + Cfg::XS * Cfg::kXBytes;
-    ParChunk *par = reinterpret_cast<ParChunk *>(cring + Cfg::CS * kStageBytes);
+    ParChunk *par = reinterpret_cast<ParChunk *>(cring + Cfg::CS * Cfg::kCodeBytes);
     const int tid = threadIdx.x, warp = warp_value(tid >> 5), lane = tid & 31, wg = warp >> 2;
-    // The codes of the first stages are asked for at once: the pack kernel
-    // let this grid launch after its own wait, so whatever ran before this
-    // call has finished.
-    Widen<NH, GROUP> widen(a, cring, wg >= 1 && wg <= Cfg::WW ? wg - 1 : 0);
-    if (wg >= 1 && wg <= Cfg::WW) widen.start();
-    if (warp == 0) tmem_alloc(&bar.tmem, kTmemCols);
-    if (warp == 1 && lane == 0) {
-        for (int i = 0; i < Cfg::XS; ++i) { mbar_init(&bar.xfull[i], 1); mbar_init(&bar.xempty[i], 1); }
-        for (int i = 0; i < kASlots; ++i) { mbar_init(&bar.afull[i], 128); mbar_init(&bar.aempty[i], 1); }
-        for (int i = 0; i < 2 * Cfg::DB; ++i) { mbar_init(&bar.dfull[i], 1); mbar_init(&bar.dempty[i], 128); }
+    CodeCopy<Cfg> codes(a, &map, bar, cring);
+    if (tid == 0) {
+        for (int i = 0; i < Cfg::CS; ++i) { mbar_init(&bar.cfull[i], 1); mbar_init(&bar.cempty[i], 4 * Cfg::WW); }
+        for (int i = 0; i < Cfg::XS; ++i) mbar_init(&bar.xfull[i], 1);
+        for (int i = 0; i < Cfg::AS; ++i) mbar_init(&bar.afull[i], 128 * Cfg::WW);
+        for (int i = 0; i < kDone; ++i) mbar_init(&bar.done[i], 1);
+        for (int i = 0; i < Cfg::AW * Cfg::DB; ++i) { mbar_init(&bar.dfull[i], 1); mbar_init(&bar.dempty[i], 128); }
         mbar_init(&bar.drain, 1);
+        fence_mbar_init();
+        // The codes of the first stages are asked for at once: the pack
+        // kernel let this grid launch after its own wait, so whatever ran
+        // before this call has finished.
+        codes.start();
     }
+    if (warp == 1) tmem_alloc(&bar.tmem, kTmemCols);
     griddep_wait();
     griddep_launch_dependents();
     const TokenPlan t = token_plan(__ldcg(a.count), a.nh_max);
-    if (warp == 1 && lane == 0) {
+    if (tid == 32) {
         for (int i = 0; i < kParSlots; ++i) {
-            mbar_init(&bar.pfull[i], 64);
+            mbar_init(&bar.pfull[i], 32);
             mbar_init(&bar.pempty[i], 4 * t.halves + (a.zero ? 4 * Cfg::WW : 0));
         }
         fence_mbar_init();
@@ -699,27 +702,28 @@ __global__ void __launch_bounds__(HeadCfg<NH>::kThreads, 1) head_kernel(HeadArgs
     if (wg == 0) {
         regs_less<Cfg::kRegs0>();
         if (warp == 0) {
-            if (lane == 0) ok = copy_role<NH>(a, t, jobs, bar, xring);
+            if (lane == 0) ok = codes.run(t, jobs);
         } else if (warp == 1) {
-            ok = mma_role<NH, GROUP>(a, t, jobs, bar, xring, tmem);
+            ok = mma_role<Cfg, NH, GROUP>(a, t, jobs, bar, xring, tmem);
+        } else if (warp == 2) {
+            if (lane == 0) ok = x_role<Cfg>(a, t, jobs, bar, xring);
         } else {
             ok = param_role(a, t, jobs, bar, par);
         }
     } else if (wg <= Cfg::WW) {
         regs_less<Cfg::kRegsW>();
-        ok = widen.run(t, jobs, bar, par, tmem);
-        cp_async_wait<0>();
+        ok = widen_role<Cfg, GROUP>(a, t, jobs, bar, cring, par, tmem, wg - 1);
     } else {
         regs_more<Cfg::kRegsA>();
         const int h = wg - 1 - Cfg::WW;
-        if (h < t.halves) ok = accumulate_role<NH>(a, t, jobs, bar, par, tmem, h);
+        if (h < t.halves) ok = accumulate_role<Cfg, NH>(a, t, jobs, bar, par, tmem, h);
     }
     if (!ok && a.status) atomicOr(a.status, SV_NOTE_TIMEOUT);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) tmem_free(tmem, kTmemCols);
+    if (warp == 1) tmem_free(tmem, kTmemCols);
 }
 
 // ---------------------------------------------------------------------------
@@ -735,46 +739,74 @@ static sv_status head_check(const sv_w4 *w, int B, int P) {
     return SV_OK;
 }
 
-// Tokens per half for a batch of at most M tokens.
-static int nh_for(int M) { return M <= 32 ? 16 : M <= 128 ? 64 : 128; }
+// Tokens per half for a batch of at most M tokens, and k per stage.
+static int nh_for(int M) { return M <= 16 ? 16 : M <= 128 ? 64 : 96; }
+static int ak_for(int nh) { return nh <= 64 ? 256 : 128; }
 
 struct HeadPlan {
     size_t off_rows, off_image, bytes;
 };
 
 static HeadPlan head_plan(const sv_w4 *w, int B, int P) {
-    const int M = B * P, nh = nh_for(M), nkb = (w->H + kStageK - 1) / kStageK;
+    const int M = B * P, nh = nh_for(M), ak = ak_for(nh), nkb = (w->H + ak - 1) / ak;
     HeadPlan p;
     auto align = [](size_t o) { return (o + 1023) & ~static_cast<size_t>(1023); };
     p.off_rows = 16;
     p.off_image = align(16 + 4ull * M);
-    // Whatever the scheduled count is, it packs into as many passes as M at
-    // most, each of at most 2 nh tokens.
-    const size_t passes = (M + 2 * nh - 1) / (2 * nh);
-    p.bytes = p.off_image + passes * 2 * nh * nkb * 256ull;
+    // Whatever the scheduled count is, it packs into at most as many passes
+    // as M does, each of at most 2 nh tokens.
+    const size_t most = nh == 16 ? 16 : 2 * nh, passes = (M + most - 1) / most;
+    p.bytes = p.off_image + passes * most * nkb * ak * 2ull;
     return p;
 }
 
+// The codes as a two-dimensional tensor of bytes, in tiles of 128 rows of one
+// stage; what lies past the matrix reads as 0.
+static cudaError_t code_map(const sv_w4 *w, int ak, CUtensorMap *map) {
+    typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                               const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static std::atomic<Encode> encode{nullptr};
+    Encode f = encode.load(std::memory_order_acquire);
+    if (!f) {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &found);
+        if (e != cudaSuccess) return e;
+        if (found != cudaDriverEntryPointSuccess || !p) return cudaErrorNotSupported;
+        f = reinterpret_cast<Encode>(p);
+        encode.store(f, std::memory_order_release);
+    }
+    const cuuint64_t dim[2] = {static_cast<cuuint64_t>(w->H / 2), static_cast<cuuint64_t>(w->V)};
+    const cuuint64_t stride[1] = {static_cast<cuuint64_t>(w->H / 2)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(ak / 2), kTileV}, step[2] = {1, 1};
+    const CUresult r = f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(w->codes), dim, stride, box, step,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         ak == 256 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <int NH, int GROUP>
-static cudaError_t launch_head(const HeadArgs &a, cudaStream_t st) {
+static cudaError_t launch_head(const HeadArgs &a, const CUtensorMap &map, cudaStream_t st) {
+    using Cfg = HeadCfg<NH, GROUP>;
     static std::atomic<bool> attr_set[64];
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess && !attr_set[dev & 63].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(head_kernel<NH, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 HeadCfg<NH>::kSmem);
+        e = cudaFuncSetAttribute(head_kernel<NH, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
         if (e == cudaSuccess) attr_set[dev & 63].store(true, std::memory_order_release);
     }
     if (e != cudaSuccess) return e;
-    return launch_pdl(head_kernel<NH, GROUP>, dim3(a.tiles < sms ? a.tiles : sms), dim3(HeadCfg<NH>::kThreads),
-                      HeadCfg<NH>::kSmem, st, a);
+    return launch_pdl(head_kernel<NH, GROUP>, dim3(a.tiles < sms ? a.tiles : sms), dim3(Cfg::kThreads), Cfg::kSmem,
+                      st, a, map);
 }
 
-template <int NH> static cudaError_t launch_group(const HeadArgs &a, cudaStream_t st) {
-    if (a.group == 128) return launch_head<NH, 128>(a, st);
-    if (a.group == 64) return launch_head<NH, 64>(a, st);
-    return launch_head<NH, 32>(a, st);
+template <int NH> static cudaError_t launch_group(const HeadArgs &a, const CUtensorMap &map, cudaStream_t st) {
+    if (a.group == 128) return launch_head<NH, 128>(a, map, st);
+    if (a.group == 64) return launch_head<NH, 64>(a, map, st);
+    return launch_head<NH, 32>(a, map, st);
 }
 
 }  // namespace sv
@@ -805,12 +837,16 @@ extern "C" sv_status sv_head_w4(const sv_w4 *weight, const void *x, int B, int P
     a.scale_f32 = weight->scale_dtype == SV_F32;
     a.out_f32 = out_dtype == SV_F32;
     a.V = weight->V; a.H = weight->H; a.group = weight->group; a.G = weight->H / weight->group;
-    a.nkb = (a.H + sv::kStageK - 1) / sv::kStageK;
     a.tiles = (a.V + sv::kTileV - 1) / sv::kTileV;
     a.x = static_cast<const __nv_bfloat16 *>(x);
     a.B = B; a.P = P; a.lengths = lengths; a.extra = extra; a.out = out;
     const int M = B * P;
     a.nh_max = sv::nh_for(M);
+    a.ak = sv::ak_for(a.nh_max);
+    a.nkb = (a.H + a.ak - 1) / a.ak;
+    CUtensorMap map;
+    cudaError_t e = sv::code_map(weight, a.ak, &map);
+    if (e != cudaSuccess) return sv::note_cuda(e);
     char *w = static_cast<char *>(workspace);
     a.count = reinterpret_cast<int *>(w);
     a.rows = reinterpret_cast<int *>(w + p.off_rows);
@@ -818,12 +854,12 @@ extern "C" sv_status sv_head_w4(const sv_w4 *weight, const void *x, int B, int P
     a.status = status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int packs = M < sv::kPackGrid ? M : sv::kPackGrid;
-    cudaError_t e = sv::launch_pdl(sv::pack_kernel, dim3(packs), dim3(sv::kPackThreads), 0, st, a);
+    e = sv::launch_pdl(sv::pack_kernel, dim3(packs), dim3(sv::kPackThreads), 0, st, a);
     if (e != cudaSuccess) return sv::note_cuda(e);
     switch (a.nh_max) {
-    case 16: e = sv::launch_group<16>(a, st); break;
-    case 64: e = sv::launch_group<64>(a, st); break;
-    default: e = sv::launch_group<128>(a, st); break;
+    case 16: e = sv::launch_group<16>(a, map, st); break;
+    case 64: e = sv::launch_group<64>(a, map, st); break;
+    default: e = sv::launch_group<96>(a, map, st); break;
     }
     return sv::note_cuda(e);
 }
