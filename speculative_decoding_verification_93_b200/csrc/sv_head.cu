@@ -173,31 +173,56 @@ __device__ __forceinline__ void tmem_alloc(uint32_t *smem, uint32_t cols) {
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
 }
-// D (fp32, tensor memory) (+)= A (bf16, tensor memory) * B (bf16, shared memory)
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)) : "memory");
+// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups
+// 1024 bytes apart; the low word holds the address.
+constexpr uint32_t kDescHigh = 64u | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t smem_desc(uint32_t addr) { return ((addr & 0x3ffffu) >> 4) | (1u << 16); }
+
+// The matrix unit's instructions are issued by one lane, elected inside the
+// statement: the warp itself never diverges, so the operands stay in uniform
+// registers and nothing has to reconverge.
+// D (fp32, tensor memory) (+)= A (bf16, tensor memory) * B (bf16, shared
+// memory), over 32 or 64 k of one swizzled block: products of 16.
+template <int K>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, bool add) {
+    if constexpr (K == 64)
+        asm volatile(
+            "{\n\t.reg .pred e, p, t;\n\t.reg .b64 b0, b1, b2, b3;\n\t.reg .b32 l1, l2, l3, c1, c2, c3;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.eq.u32 t, %4, %4;\n\t"
+            "add.u32 l1, %2, 2;\n\tadd.u32 l2, %2, 4;\n\tadd.u32 l3, %2, 6;\n\t"
+            "add.u32 c1, %1, 8;\n\tadd.u32 c2, %1, 16;\n\tadd.u32 c3, %1, 24;\n\t"
+            "mov.b64 b0, {%2, %3};\n\tmov.b64 b1, {l1, %3};\n\tmov.b64 b2, {l2, %3};\n\tmov.b64 b3, {l3, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b0, %4, p;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [c1], b1, %4, t;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [c2], b2, %4, t;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [c3], b3, %4, t;\n\t}"
+            ::"r"(d), "r"(a), "r"(b_lo), "n"(kDescHigh), "r"(idesc), "r"(static_cast<uint32_t>(add)) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred e, p, t;\n\t.reg .b64 b0, b1;\n\t.reg .b32 l1, c1;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.eq.u32 t, %4, %4;\n\t"
+            "add.u32 l1, %2, 2;\n\tadd.u32 c1, %1, 8;\n\tmov.b64 b0, {%2, %3};\n\tmov.b64 b1, {l1, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b0, %4, p;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [c1], b1, %4, t;\n\t}"
+            ::"r"(d), "r"(a), "r"(b_lo), "n"(kDescHigh), "r"(idesc), "r"(static_cast<uint32_t>(add)) : "memory");
 }
-// `bar` completes one arrival when every mma issued so far has finished.
+// `bar` completes one arrival when every product issued so far has finished.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                 ::"r"(smem_u32(bar)) : "memory");
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+        ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
         ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&f)[16]) {
@@ -208,6 +233,19 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&f)[16]) {
           "=f"(f[8]), "=f"(f[9]), "=f"(f[10]), "=f"(f[11]), "=f"(f[12]), "=f"(f[13]), "=f"(f[14]), "=f"(f[15])
         : "r"(addr) : "memory");
 }
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&f)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7]),
+          "=f"(f[8]), "=f"(f[9]), "=f"(f[10]), "=f"(f[11]), "=f"(f[12]), "=f"(f[13]), "=f"(f[14]), "=f"(f[15]),
+          "=f"(f[16]), "=f"(f[17]), "=f"(f[18]), "=f"(f[19]), "=f"(f[20]), "=f"(f[21]), "=f"(f[22]), "=f"(f[23]),
+          "=f"(f[24]), "=f"(f[25]), "=f"(f[26]), "=f"(f[27]), "=f"(f[28]), "=f"(f[29]), "=f"(f[30]), "=f"(f[31])
+        : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&f)[16]) { tmem_ld16(addr, f); }
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&f)[32]) { tmem_ld32(addr, f); }
 // Loads from tensor memory land by the wait; naming their registers here
 // keeps every use behind it.
 __device__ __forceinline__ void tc_wait_ld(float (&f)[16]) {
@@ -215,6 +253,15 @@ __device__ __forceinline__ void tc_wait_ld(float (&f)[16]) {
                  : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3]), "+f"(f[4]), "+f"(f[5]), "+f"(f[6]), "+f"(f[7]),
                    "+f"(f[8]), "+f"(f[9]), "+f"(f[10]), "+f"(f[11]), "+f"(f[12]), "+f"(f[13]), "+f"(f[14]), "+f"(f[15])
                  :: "memory");
+}
+__device__ __forceinline__ void tc_wait_ld(float (&f)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3]), "+f"(f[4]), "+f"(f[5]), "+f"(f[6]), "+f"(f[7]),
+                   "+f"(f[8]), "+f"(f[9]), "+f"(f[10]), "+f"(f[11]), "+f"(f[12]), "+f"(f[13]), "+f"(f[14]), "+f"(f[15]),
+                   "+f"(f[16]), "+f"(f[17]), "+f"(f[18]), "+f"(f[19]), "+f"(f[20]), "+f"(f[21]), "+f"(f[22]), "+f"(f[23]),
+                   "+f"(f[24]), "+f"(f[25]), "+f"(f[26]), "+f"(f[27]), "+f"(f[28]), "+f"(f[29]), "+f"(f[30])
+                 :: "memory");
+    asm volatile("" : "+f"(f[31]));
 }
 template <int N> __device__ __forceinline__ void regs_less() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -228,13 +275,6 @@ __device__ __forceinline__ void tma_tile(void *dst, const CUtensorMap *map, int 
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
         ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
-}
-
-// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups
-// 1024 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
-    return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
-           (2ull << 61);
 }
 
 // ---------------------------------------------------------------------------
@@ -271,18 +311,23 @@ template <int NH, int GROUP> struct HeadCfg {
     static constexpr int AW = NH <= 16 ? 1 : 2;
     static constexpr int GB = NH <= 16 ? AK / GROUP : 1;
     static constexpr int DB = NH <= 16 ? (GROUP == 32 ? 2 : 4) : 2;
-    static constexpr int XS = NH <= 16 ? 4 : NH <= 64 ? 2 : 3;
-    static constexpr int CS = NH <= 16 ? 8 : NH <= 64 ? 4 : 5;
+    static constexpr int XS = NH <= 16 ? 4 : 2;
+    static constexpr int CS = NH <= 16 ? 8 : NH <= 64 ? 4 : 8;
     static constexpr int kSubs = AK / GROUP;
+    static constexpr int kBatches = kSubs / GB;      // of one half in a stage
+    // Columns read back at once (twice that many registers).
+    static constexpr int kLoad = NH <= 16 ? 16 : NH <= 64 ? 16 : 32;
     static constexpr int kACol = AW * DB * GB * NH;
     static constexpr int kThreads = 128 * (1 + WW + AW);
     // Registers a thread of the service, widening and accumulating
     // warpgroups: their sum stays within what the CTA was launched with.
+    // With one accumulating warpgroup the launch's 128 do for every role.
+    static constexpr bool kSplit = NH > 16;
     static constexpr int kRegs0 = 72;
-    static constexpr int kRegsW = NH <= 16 ? 96 : NH <= 64 ? 80 : 72;
-    static constexpr int kRegsA = NH <= 16 ? 136 : NH <= 64 ? 120 : 184;
+    static constexpr int kRegsW = NH <= 64 ? 80 : 72;
+    static constexpr int kRegsA = NH <= 64 ? 120 : 184;
     static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
-    static_assert(kRegs0 + WW * kRegsW + AW * kRegsA <= (1 + WW + AW) * kLaunchRegs, "register split");
+    static_assert(!kSplit || kRegs0 + WW * kRegsW + AW * kRegsA <= (1 + WW + AW) * kLaunchRegs, "register split");
     static constexpr int kCodeBytes = kTileV * AK / 2;
     static constexpr int kXBytes = AW * NH * AK * 2;
     // At least half of the SM's shared memory: two CTAs on one SM would
@@ -291,7 +336,7 @@ template <int NH, int GROUP> struct HeadCfg {
                                  kParSlots * static_cast<int>(sizeof(ParChunk));
     static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
     static_assert(kSmem <= 227 * 1024 - 1024 && kACol + AS * AK / 2 <= static_cast<int>(kTmemCols), "head layout");
-    static_assert(XS < kDone && AS < kDone && 2 + AW <= 32 && kParGroups % GB == 0, "head rings");
+    static_assert(XS < kDone && AS < kDone && AS % WW == 0 && kParGroups % GB == 0, "head rings");
 };
 
 struct HeadBars {
@@ -301,19 +346,20 @@ struct HeadBars {
     uint64_t done[kDone];                // the matrix unit is through a stage: its x and A are free
     uint64_t dfull[8], dempty[8];        // a batch finished; read back
     uint64_t pfull[kParSlots], pempty[kParSlots];
-    uint64_t drain;
     uint32_t tmem;
 };
 
-// A warp-wide bounded wait: every lane gets the same answer.
+// Bounded wait, warp-wide: every lane gets the same answer.  One compact loop:
+// five roles share each scheduler's instruction cache, and a role's pace is
+// set by how much of its code has to be fetched again.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, kHeadWaitNs));
-}
-
-__device__ __forceinline__ bool elect_one() {
-    uint32_t e;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
-    return e != 0;
+    uint64_t t0 = 0;
+    while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+        const uint64_t now = global_ns();
+        if (t0 == 0) t0 = now;
+        if (__any_sync(0xffffffffu, now - t0 > kHeadWaitNs)) return false;
+    }
+    return true;
 }
 
 __device__ __forceinline__ int warp_value(int v) { return __shfl_sync(0xffffffffu, v, 0); }
@@ -394,65 +440,67 @@ __device__ bool x_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars
     return ok;
 }
 
-// The matrix unit's instructions (warp 1: every lane runs the loops, so that
-// the operands stay in uniform registers; one lane issues).  What a batch
-// waits for is waited for at once, one barrier a lane: each wait costs some
-// 80 cycles even when nothing is missing, more than the eight instructions
-// of a batch.
+// The matrix unit's instructions (warp 1, all lanes together).  Every
+// stage has all its batches; one past the last group has no products.
 template <typename Cfg, int NH, int GROUP>
 __device__ bool mma_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars &bar, const char *xring,
                          uint32_t tmem) {
-    constexpr int kBatches = Cfg::kSubs / Cfg::GB;   // of one half in a stage
-    const int lane = threadIdx.x & 31;
-    const uint32_t nh = warp_value(t.nh);
-    const int halves = warp_value(t.halves), stages = warp_value(jobs) * a.nkb;
+    const uint32_t nh = warp_value(t.nh), nh8 = nh * 8;
+    const int halves = warp_value(t.halves);
+    const int stages = warp_value(jobs) * a.nkb, last_subs = (a.H - (a.nkb - 1) * Cfg::AK) / GROUP;
     const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((nh >> 3) << 17) | ((kTileV >> 4) << 24);
-    const uint64_t x0 = smem_desc(smem_u32(xring));
-    const bool issuer = elect_one();
-    int i = 0, kb = 0;                    // batch of a half (counts through all jobs), stage of the job
+    const uint32_t x0 = smem_desc(smem_u32(xring));
+    constexpr int kUnit = GROUP < 64 ? GROUP : 64;
+    int left = a.nkb;                     // stages of the job still to come
+    uint32_t i = 0;                       // batch of a half
     bool ok = true;
-    for (int s = 0; s < stages; ++s) {
-        const int ab = s % Cfg::AS, slot = s % Cfg::XS;
-        const int subs = min(Cfg::kSubs, (a.H - kb * Cfg::AK) / GROUP);
-        const uint64_t xs = x0 + static_cast<uint64_t>(slot * (Cfg::kXBytes / 16));
-        const uint32_t acol = tmem + Cfg::kACol + ab * (Cfg::AK / 2);
-#pragma unroll
-        for (int j = 0; j < kBatches; ++j) {
-            if (j * Cfg::GB >= subs) break;
-            const int d = i % Cfg::DB;
-            uint64_t *b = &bar.dempty[(lane & 1 ? halves - 1 : 0) * Cfg::DB + d];
-            uint32_t parity = ((i / Cfg::DB) & 1) ^ 1;
-            if (j == 0 && lane == 2) { b = &bar.afull[ab]; parity = (s / Cfg::AS) & 1; }
-            if (j == 0 && lane == 3) { b = &bar.xfull[slot]; parity = (s / Cfg::XS) & 1; }
-            if (!warp_wait(b, parity)) { ok = false; break; }
+#pragma unroll 1
+    for (uint32_t s = 0; ok && s < static_cast<uint32_t>(stages); ++s) {
+        const uint32_t ab = s % Cfg::AS, slot = s % Cfg::XS;
+        const int subs = left == 1 ? last_subs : Cfg::kSubs;
+        const uint32_t xs = x0 + slot * (Cfg::kXBytes / 16);
+        uint32_t acol = tmem + Cfg::kACol + ab * (Cfg::AK / 2);
+        int k32 = 0;                      // 32-k blocks into the stage
+        if (!warp_wait(&bar.xfull[slot], (s / Cfg::XS) & 1) || !warp_wait(&bar.afull[ab], (s / Cfg::AS) & 1)) {
+            ok = false;
+            break;
+        }
+#pragma unroll 1
+        for (int j = 0; j < Cfg::kBatches; ++j, ++i) {
+            const uint32_t d = i % Cfg::DB;
+            const uint32_t parity = ((i / Cfg::DB) & 1) ^ 1;
+            if (!warp_wait(&bar.dempty[d], parity) ||
+                (halves == 2 && !warp_wait(&bar.dempty[(Cfg::AW - 1) * Cfg::DB + d], parity))) { ok = false; break; }
             tc_fence_after();
-            if (issuer) {
-                for (int h = 0; h < halves; ++h) {
-                    const int db = h * Cfg::DB + d;
-                    const uint64_t xh = xs + static_cast<uint64_t>(h * (Cfg::AK / 64) * nh * 8);
+            const int live = min(Cfg::GB, subs - j * Cfg::GB);   // groups of the batch
+#pragma unroll 1
+            for (int h = 0; h < halves; ++h) {
+                uint32_t acc = tmem + (h * Cfg::DB + d) * Cfg::GB * NH;
+                const uint32_t xh = xs + h * (Cfg::AK / 64) * nh8;
 #pragma unroll
-                    for (int q = 0; q < Cfg::GB * GROUP / 16; ++q) {
-                        const int k16 = j * (Cfg::GB * GROUP / 16) + q, g = q / (GROUP / 16);
-                        if (Cfg::GB > 1 && j * Cfg::GB + g >= subs) break;
-                        mma_ts(tmem + (db * Cfg::GB + g) * NH, acol + 8 * k16,
-                               xh + (k16 >> 2) * nh * 8 + (k16 & 3) * 2, idesc, q % (GROUP / 16) > 0);
+                for (int g = 0; g < Cfg::GB; ++g, acc += NH) {
+                    if (g >= live) break;
+#pragma unroll
+                    for (int w = 0; w < GROUP / kUnit; ++w) {
+                        const int k = k32 + (g * GROUP + w * kUnit) / 32;   // 32-k block of the stage
+                        mma_ts<kUnit>(acc, acol + 16 * (k - k32), xh + (k >> 1) * nh8 + (k & 1) * 4, idesc, w > 0);
                     }
-                    mma_commit(&bar.dfull[db]);
                 }
+                mma_commit(&bar.dfull[h * Cfg::DB + d]);
             }
-            __syncwarp();
-            ++i;
+            acol += Cfg::GB * GROUP / 2;
+            k32 += Cfg::GB * GROUP / 32;
         }
         if (!ok) break;
-        if (issuer) mma_commit(&bar.done[s % kDone]);
-        __syncwarp();
-        if (++kb == a.nkb) kb = 0;
+        mma_commit(&bar.done[s % kDone]);
+        if (--left == 0) left = a.nkb;
     }
-    // Nothing of the matrix unit is in flight when tensor memory is freed.
-    if (issuer) mma_commit(&bar.drain);
-    __syncwarp();
-    warp_wait(&bar.drain, 0);
-    return ok;
+    // Nothing of the matrix unit is in flight when tensor memory is freed: the
+    // last stage's commit covers all before it.  After a wait that ran out,
+    // a millisecond is far more than what was issued needs.
+    if (!ok)
+        for (const uint64_t t0 = global_ns(); global_ns() - t0 < 1000000;) __nanosleep(1000);
+    return ok && (stages == 0 || warp_wait(&bar.done[(stages - 1) % kDone], ((stages - 1) / kDone) & 1));
 }
 
 // Scales and zero points (warp 3, four rows a lane): as fp32 and bf16 pairs
@@ -512,19 +560,20 @@ __device__ bool param_role(const HeadArgs &a, const TokenPlan &t, int jobs, Head
     return true;
 }
 
-// One of WW warpgroups: its share of every stage's k (128), one weight row a
-// thread.
+// One of WW warpgroups: the stages s = wi mod WW, one weight row a thread, 128 k
+// (a step) at a time.  The next step's codes are read from shared memory while
+// this step's are widened.
 template <typename Cfg, int GROUP>
 __device__ bool widen_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars &bar, const char *ring,
                            const ParChunk *par, uint32_t tmem, int wi) {
-    constexpr int kRowBytes = Cfg::AK / 2, kMine = 128 / GROUP;   // groups of this share
+    constexpr int kRowBytes = Cfg::AK / 2, kSteps = Cfg::AK / 128, kMine = 128 / GROUP;   // groups of a step
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
     const int stages = jobs * a.nkb, chunks = (a.G + kParGroups - 1) / kParGroups;
     const int r = quarter * 32 + lane;
     // The copy's swizzle: 16-byte pieces of 128-byte (64-byte) rows.
     const int swz = kRowBytes == 128 ? r & 7 : (r >> 1) & 3;
-    const uint32_t dst0 = tmem + Cfg::kACol + wi * 64 + (static_cast<uint32_t>(quarter * 32) << 16);
-    int kb = 0, c0 = 0, have = -1;        // stage of the job, chunks before the job, chunk at hand
+    const uint32_t dst0 = tmem + Cfg::kACol + (static_cast<uint32_t>(quarter * 32) << 16);
+    int kb = wi, c0 = 0, have = -1;       // stage of the job, chunks before the job, chunk at hand
     uint32_t off[kMine];
 #pragma unroll
     for (int g = 0; g < kMine; ++g) off[g] = zero_pair(8);
@@ -533,55 +582,77 @@ __device__ bool widen_role(const HeadArgs &a, const TokenPlan &t, int jobs, Head
         if (have >= 0) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.pempty[have % kParSlots]);
+            __syncwarp();
         }
         ++have;
         return !wait || warp_wait(&bar.pfull[have % kParSlots], (have / kParSlots) & 1);
     };
-    for (int s = 0; s < stages; ++s) {
-        const int slot = s % Cfg::CS, ab = s % Cfg::AS, old = s - Cfg::AS;
-        if (!warp_wait(&bar.cfull[slot], (s / Cfg::CS) & 1)) return false;
+    uint4 u[4];                           // the codes of the step at hand
+    auto load = [&](uint4 (&to)[4], int s, int step) {
+        const int slot = s % Cfg::CS;
+        if (step == 0 && !warp_wait(&bar.cfull[slot], (s / Cfg::CS) & 1)) return false;
         const char *row = ring + slot * Cfg::kCodeBytes + r * kRowBytes;
-        uint4 u[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) u[j] = *reinterpret_cast<const uint4 *>(row + (((4 * wi + j) ^ swz) * 16));
-        if (a.zero) {
+        for (int j = 0; j < 4; ++j) to[j] = *reinterpret_cast<const uint4 *>(row + (((4 * step + j) ^ swz) * 16));
+        return true;
+    };
+    if (wi < stages && !load(u, wi, 0)) return false;
+#pragma unroll 1
+    for (int s = wi; s < stages; s += Cfg::WW) {
+        const int ab = s % Cfg::AS, old = s - Cfg::AS;
+        while (kb >= a.nkb) { kb -= a.nkb; c0 += chunks; }
+#pragma unroll 1
+        for (int step = 0; step < kSteps; ++step) {
+            const bool last = step == kSteps - 1;
+            uint4 next[4] = {u[0], u[1], u[2], u[3]};
+            if (!last || s + Cfg::WW < stages)
+                if (!load(next, last ? s + Cfg::WW : s, last ? 0 : step + 1)) return false;
+            if (a.zero) {
 #pragma unroll
-            for (int g = 0; g < kMine; ++g) {
-                const int gi = min(kb * Cfg::kSubs + wi * kMine + g, a.G - 1), c = c0 + gi / kParGroups;
-                while (have < c)
-                    if (!next_chunk(true)) return false;
-                off[g] = par[c % kParSlots].off[gi % kParGroups][r];
+                for (int g = 0; g < kMine; ++g) {
+                    const int gi = min(kb * Cfg::kSubs + step * kMine + g, a.G - 1), c = c0 + gi / kParGroups;
+                    while (have < c)
+                        if (!next_chunk(true)) return false;
+                    off[g] = par[c % kParSlots].off[gi % kParGroups][r];
+                }
             }
-        }
-        if (old >= 0 && !warp_wait(&bar.done[old % kDone], (old / kDone) & 1)) return false;
-        tc_fence_after();
+            if (step == 0 && old >= 0 && !warp_wait(&bar.done[old % kDone], (old / kDone) & 1)) return false;
+            tc_fence_after();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t w[32];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint4 &v = u[2 * h + j];
-                const uint32_t o = off[(2 * h + j) * 32 / GROUP];
-                widen8(v.x, o, w + j * 16);
-                widen8(v.y, o, w + j * 16 + 4);
-                widen8(v.z, o, w + j * 16 + 8);
-                widen8(v.w, o, w + j * 16 + 12);
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t o = off[j * 32 / GROUP];
+                uint32_t w[16];
+                widen8(u[j].x, o, w);
+                widen8(u[j].y, o, w + 4);
+                widen8(u[j].z, o, w + 8);
+                widen8(u[j].w, o, w + 12);
+                tmem_st16(dst0 + ab * (Cfg::AK / 2) + step * 64 + j * 16, w);
             }
-            tmem_st32(dst0 + ab * (Cfg::AK / 2) + h * 32, w);
+            if (last) {
+                // A is written, and the stage's codes (all steps) were read
+                // into registers in every lane.
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bar.afull[ab]);
+                    mbar_arrive(&bar.cempty[s % Cfg::CS]);
+                }
+                __syncwarp();
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[j] = next[j];
         }
-        // The codes are in registers in every lane of this warp.
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.cempty[slot]);
-        tc_wait_st();
-        tc_fence_before();
-        mbar_arrive(&bar.afull[ab]);
-        if (++kb == a.nkb) { kb = 0; c0 += chunks; }
+        kb += Cfg::WW;
     }
     if (a.zero)
         for (const int all = jobs * chunks; have < all;)
             if (!next_chunk(have + 1 < all)) return false;
     return true;
 }
+
+__device__ __forceinline__ void store_logit(float *p, float z) { *p = z; }
+__device__ __forceinline__ void store_logit(__nv_bfloat16 *p, float z) { *p = __float2bfloat16_rn(z); }
 
 // One warpgroup per half of the tokens; a thread owns one vocabulary row.
 template <typename Cfg, int NH>
@@ -602,56 +673,77 @@ __device__ bool accumulate_role(const HeadArgs &a, const TokenPlan &t, int jobs,
         float acc[NH];
 #pragma unroll
         for (int n = 0; n < NH; ++n) acc[n] = 0.f;
-        for (int g0 = 0; g0 < a.G; g0 += kParGroups, ++c) {
-            const int slot = c % kParSlots, ng = min(kParGroups, a.G - g0);
-            if (!warp_wait(&bar.pfull[slot], (c / kParSlots) & 1)) return false;
-            for (int q0 = 0; q0 < ng; q0 += Cfg::GB, ++i) {
-                const int db = h * Cfg::DB + i % Cfg::DB;
+#pragma unroll 1
+        for (int kb = 0; kb < a.nkb; ++kb) {
+#pragma unroll 1
+            for (int j = 0; j < Cfg::kBatches; ++j, ++i) {
+                const int gi = kb * Cfg::kSubs + j * Cfg::GB, db = h * Cfg::DB + i % Cfg::DB;
+                const int slot = c % kParSlots;
+                if (gi % kParGroups == 0 && gi < a.G && !warp_wait(&bar.pfull[slot], (c / kParSlots) & 1)) return false;
                 if (!warp_wait(&bar.dfull[db], (i / Cfg::DB) & 1)) return false;
                 tc_fence_after();
+                if (gi < a.G) {
+                    const float *scale = &par[slot].scale[gi % kParGroups][quarter * 32 + lane];
+                    const uint32_t src = lanes + db * Cfg::GB * NH;
+                    // Blocks of kLoad columns, groups outside; the next block
+                    // is on its way while one is added.
+                    constexpr int kBlocks = NH / Cfg::kLoad;
+                    float d[2][Cfg::kLoad];
+                    tmem_ld(src, d[0]);
 #pragma unroll
-                for (int q = 0; q < Cfg::GB; ++q) {
-                    if (Cfg::GB > 1 && q0 + q >= ng) break;
-                    const float sc = par[slot].scale[q0 + q][quarter * 32 + lane];
-                    const float2 ss = make_float2(sc, sc);
-                    const uint32_t src = lanes + (db * Cfg::GB + q) * NH;
-                    // The next 16 columns are on their way while these are added.
-                    float d[2][16];
-                    tmem_ld16(src, d[0]);
+                    for (int q = 0; q < Cfg::GB; ++q) {
+                        if (Cfg::GB > 1 && gi + q >= a.G) break;
+                        const float sc = scale[q * kTileV];
+                        const float2 ss = make_float2(sc, sc);
 #pragma unroll
-                    for (int k = 0; k < NH / 16; ++k) {
-                        if (16 * k < t.nh) {
-                            tc_wait_ld(d[k & 1]);
-                            if (k + 1 < NH / 16 && 16 * (k + 1) < t.nh)
-                                tmem_ld16(src + 16 * (k + 1), d[(k + 1) & 1]);
+                        for (int k = 0; k < kBlocks; ++k) {
+                            if (Cfg::kLoad * k < t.nh) {
+                                const int at = q * kBlocks + k;
+                                tc_wait_ld(d[at & 1]);
+                                if (k + 1 < kBlocks && Cfg::kLoad * (k + 1) < t.nh)
+                                    tmem_ld(src + q * NH + Cfg::kLoad * (k + 1), d[(at + 1) & 1]);
+                                else if (kBlocks == 1 && q + 1 < Cfg::GB)
+                                    tmem_ld(src + (q + 1) * NH, d[(at + 1) & 1]);
 #pragma unroll
-                            for (int n = 0; n < 16; n += 2) {
-                                float *y = acc + 16 * k + n;
-                                const float2 z = __ffma2_rn(make_float2(d[k & 1][n], d[k & 1][n + 1]), ss,
-                                                            make_float2(y[0], y[1]));
-                                y[0] = z.x;
-                                y[1] = z.y;
+                                for (int n = 0; n < Cfg::kLoad; n += 2) {
+                                    float *y = acc + Cfg::kLoad * k + n;
+                                    const float2 z = __ffma2_rn(make_float2(d[at & 1][n], d[at & 1][n + 1]), ss,
+                                                                make_float2(y[0], y[1]));
+                                    y[0] = z.x;
+                                    y[1] = z.y;
+                                }
                             }
                         }
                     }
+                    // A group's last load may still be in flight (of a group past the end).
+                    tc_wait_ld(d[0]);
                 }
                 tc_fence_before();
-                mbar_arrive(&bar.dempty[db]);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.pempty[slot]);
-        }
-        // One vocabulary row per lane: a warp writes 32 consecutive logits of each token.
-#pragma unroll
-        for (int n = 0; n < NH; ++n) {
-            if (n < live) {
-                const long long at = static_cast<long long>(__shfl_sync(0xffffffffu, rows[n / 32], n % 32)) * a.V + v;
-                if (v < a.V) {
-                    if (a.out_f32) static_cast<float *>(a.out)[at] = acc[n];
-                    else static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(acc[n]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.dempty[db]);
+                if (gi < a.G && ((gi + Cfg::GB) % kParGroups == 0 || gi + Cfg::GB >= a.G)) {
+                    if (lane == 0) mbar_arrive(&bar.pempty[slot]);
+                    ++c;
                 }
             }
         }
+        // One vocabulary row per lane: a warp writes 32 consecutive logits of each token.
+        auto write = [&](auto *out) {
+#pragma unroll
+            for (int n0 = 0; n0 < NH; n0 += 4) {
+                if (n0 < live) {
+                    decltype(out) to[4];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+                        to[n] = out + static_cast<long long>(__shfl_sync(0xffffffffu, rows[(n0 + n) / 32], (n0 + n) % 32)) * a.V;
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+                        if (n0 + n < live && v < a.V) store_logit(to[n], acc[n0 + n]);
+                }
+            }
+        };
+        if (a.out_f32) write(static_cast<float *>(a.out) + v);
+        else write(static_cast<__nv_bfloat16 *>(a.out) + v);
     }
     return true;
 }
@@ -668,12 +760,11 @@ head_kernel(HeadArgs a, const __grid_constant__ CUtensorMap map) {
     const int tid = threadIdx.x, warp = warp_value(tid >> 5), lane = tid & 31, wg = warp >> 2;
     CodeCopy<Cfg> codes(a, &map, bar, cring);
     if (tid == 0) {
-        for (int i = 0; i < Cfg::CS; ++i) { mbar_init(&bar.cfull[i], 1); mbar_init(&bar.cempty[i], 4 * Cfg::WW); }
+        for (int i = 0; i < Cfg::CS; ++i) { mbar_init(&bar.cfull[i], 1); mbar_init(&bar.cempty[i], 4); }
         for (int i = 0; i < Cfg::XS; ++i) mbar_init(&bar.xfull[i], 1);
-        for (int i = 0; i < Cfg::AS; ++i) mbar_init(&bar.afull[i], 128 * Cfg::WW);
+        for (int i = 0; i < Cfg::AS; ++i) mbar_init(&bar.afull[i], 4);
         for (int i = 0; i < kDone; ++i) mbar_init(&bar.done[i], 1);
-        for (int i = 0; i < Cfg::AW * Cfg::DB; ++i) { mbar_init(&bar.dfull[i], 1); mbar_init(&bar.dempty[i], 128); }
-        mbar_init(&bar.drain, 1);
+        for (int i = 0; i < Cfg::AW * Cfg::DB; ++i) { mbar_init(&bar.dfull[i], 1); mbar_init(&bar.dempty[i], 4); }
         fence_mbar_init();
         // The codes of the first stages are asked for at once: the pack
         // kernel let this grid launch after its own wait, so whatever ran
@@ -700,7 +791,7 @@ head_kernel(HeadArgs a, const __grid_constant__ CUtensorMap map) {
     const int jobs = my_tiles * t.passes;
     bool ok = true;
     if (wg == 0) {
-        regs_less<Cfg::kRegs0>();
+        if constexpr (Cfg::kSplit) regs_less<Cfg::kRegs0>();
         if (warp == 0) {
             if (lane == 0) ok = codes.run(t, jobs);
         } else if (warp == 1) {
@@ -711,10 +802,10 @@ head_kernel(HeadArgs a, const __grid_constant__ CUtensorMap map) {
             ok = param_role(a, t, jobs, bar, par);
         }
     } else if (wg <= Cfg::WW) {
-        regs_less<Cfg::kRegsW>();
+        if constexpr (Cfg::kSplit) regs_less<Cfg::kRegsW>();
         ok = widen_role<Cfg, GROUP>(a, t, jobs, bar, cring, par, tmem, wg - 1);
     } else {
-        regs_more<Cfg::kRegsA>();
+        if constexpr (Cfg::kSplit) regs_more<Cfg::kRegsA>();
         const int h = wg - 1 - Cfg::WW;
         if (h < t.halves) ok = accumulate_role<Cfg, NH>(a, t, jobs, bar, par, tmem, h);
     }
