@@ -585,7 +585,7 @@ def sv_head_w4_workspace_bytes(weight: W4Weight, B: int, P: int) -> int:
     return int(lib().sv_head_w4_workspace_bytes(weight.desc, B, P))
 
 
-def sv_head_w4(weight: W4Weight, x, out, workspace, lengths=None, extra: int = 0, status=None,
+def sv_head_w4(weight: W4Weight, x, out, workspace=None, lengths=None, extra: int = 0, status=None,
                stream=None) -> None:
     """out [B, P, V] (float32 or bfloat16) = x [B, P, H] (bfloat16) times the
     4-bit weights; positions p >= lengths[b] + extra are left as they were."""
@@ -597,8 +597,8 @@ def sv_head_w4(weight: W4Weight, x, out, workspace, lengths=None, extra: int = 0
     _call("sv_head_w4", x, stream, weight.desc, _given(x, torch.bfloat16, "x", x), B, P,
           _given(lengths, torch.int32, "lengths", x, (B,)), int(extra),
           _given(out, out.dtype, "out", x, (B, P, weight.V)), _dtype(out),
-          _given(workspace, workspace.dtype, "workspace", x),
-          workspace.numel() * workspace.element_size(),
+          None if workspace is None else _given(workspace, workspace.dtype, "workspace", x),
+          0 if workspace is None else workspace.numel() * workspace.element_size(),
           _given(status, torch.int32, "status", x))
 
 

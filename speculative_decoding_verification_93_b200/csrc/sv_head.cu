@@ -51,11 +51,10 @@ struct TokenPlan {
     int count, passes, per, halves, nh;
 };
 
-// nh_max 16 takes at most 16 tokens, in one half.
 __host__ __device__ __forceinline__ TokenPlan token_plan(int count, int nh_max) {
     TokenPlan p;
     p.count = count;
-    const int most = nh_max == 16 ? 16 : 2 * nh_max;
+    const int most = 2 * nh_max;
     p.passes = (count + most - 1) / most;
     const int share = p.passes ? (count + p.passes - 1) / p.passes : 0;
     p.halves = share <= 16 ? 1 : 2;
@@ -295,56 +294,49 @@ struct ParChunk {
 
 // Up to NH tokens a half, for weights in groups of GROUP.  AK k per stage, AS
 // A operands in tensor memory (AK / 2 columns each, behind the accumulators),
-// CS and XS stages of codes and x in shared memory, WW warpgroups that widen,
-// AW that accumulate.  A batch is GB groups of one half; DB batches of a half
-// are in tensor memory at a time.
-//   NH = 16: waiting is all that costs, so a batch is a whole stage.
-//   NH = 64: a stage of 256 k, whose widening two warpgroups share.
-//   NH = 96: the matrix unit sets the pace (8 nh cycles for 128 k; one
-//   warpgroup widens that in about 450), and needs two batches a half so that
-//   it never waits for the read-back: 384 columns, which leaves A two stages
-//   of 128 k.
+// CS and XS stages of codes and x in shared memory, WW warpgroups that widen.
+// A batch is one group of one half; DB batches of a half are in tensor memory
+// at a time.
+//   NH = 64: stages of 256 k, which two warpgroups widen in turn.
+//   NH = 96: the matrix unit sets the pace (8 nh cycles for 128 k of both
+//   halves; one warpgroup widens that in about 600), and the accumulators
+//   need the registers of a second one.  384 columns of batches leave A two
+//   stages of 128 k.
 template <int NH, int GROUP> struct HeadCfg {
     static constexpr int AK = NH <= 64 ? 256 : 128;
     static constexpr int AS = 2;
     static constexpr int WW = NH <= 64 ? 2 : 1;
-    static constexpr int AW = NH <= 16 ? 1 : 2;
-    static constexpr int GB = NH <= 16 ? AK / GROUP : 1;
-    static constexpr int DB = NH <= 16 ? (GROUP == 32 ? 2 : 4) : 2;
-    static constexpr int XS = NH <= 16 ? 4 : 2;
-    static constexpr int CS = NH <= 16 ? 8 : NH <= 64 ? 4 : 8;
+    static constexpr int DB = 2;
+    static constexpr int XS = 2;
+    static constexpr int CS = NH <= 64 ? 4 : 8;
     static constexpr int kSubs = AK / GROUP;
-    static constexpr int kBatches = kSubs / GB;      // of one half in a stage
-    // Columns read back at once (twice that many registers).
-    static constexpr int kLoad = NH <= 16 ? 16 : NH <= 64 ? 16 : 32;
-    static constexpr int kACol = AW * DB * GB * NH;
-    static constexpr int kThreads = 128 * (1 + WW + AW);
+    static constexpr int kLoad = NH <= 64 ? 16 : 32;   // columns read back at once (twice that many registers)
+    static constexpr int kACol = 2 * DB * NH;
+    static constexpr int kThreads = 128 * (3 + WW);
     // Registers a thread of the service, widening and accumulating
     // warpgroups: their sum stays within what the CTA was launched with.
-    // With one accumulating warpgroup the launch's 128 do for every role.
-    static constexpr bool kSplit = NH > 16;
     static constexpr int kRegs0 = 72;
     static constexpr int kRegsW = NH <= 64 ? 80 : 72;
     static constexpr int kRegsA = NH <= 64 ? 120 : 184;
     static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
-    static_assert(!kSplit || kRegs0 + WW * kRegsW + AW * kRegsA <= (1 + WW + AW) * kLaunchRegs, "register split");
+    static_assert(kRegs0 + WW * kRegsW + 2 * kRegsA <= (3 + WW) * kLaunchRegs, "register split");
     static constexpr int kCodeBytes = kTileV * AK / 2;
-    static constexpr int kXBytes = AW * NH * AK * 2;
-    // At least half of the SM's shared memory: two CTAs on one SM would
+    static constexpr int kXBytes = 2 * NH * AK * 2;
+    // More than half of the SM's shared memory, as two CTAs on one SM would
     // wait for each other's tensor memory.
-    static constexpr int kUsed = 1024 + XS * kXBytes + CS * kCodeBytes +
+    static constexpr int kSmem = 1024 + XS * kXBytes + CS * kCodeBytes +
                                  kParSlots * static_cast<int>(sizeof(ParChunk));
-    static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
-    static_assert(kSmem <= 227 * 1024 - 1024 && kACol + AS * AK / 2 <= static_cast<int>(kTmemCols), "head layout");
-    static_assert(XS < kDone && AS < kDone && AS % WW == 0 && kParGroups % GB == 0, "head rings");
+    static_assert(kSmem > 120 * 1024 && kSmem <= 227 * 1024 - 1024, "shared memory");
+    static_assert(kACol + AS * AK / 2 <= static_cast<int>(kTmemCols), "tensor memory");
+    static_assert(XS < kDone && AS < kDone && AS % WW == 0, "rings");
 };
 
 struct HeadBars {
     uint64_t cfull[8], cempty[8];        // codes landed; read by the widening warps
-    uint64_t xfull[4];                   // x landed
+    uint64_t xfull[2];                   // x landed
     uint64_t afull[2];                   // A written
     uint64_t done[kDone];                // the matrix unit is through a stage: its x and A are free
-    uint64_t dfull[8], dempty[8];        // a batch finished; read back
+    uint64_t dfull[4], dempty[4];        // a batch finished; read back
     uint64_t pfull[kParSlots], pempty[kParSlots];
     uint32_t tmem;
 };
@@ -382,6 +374,11 @@ __device__ __forceinline__ void widen8(uint32_t w, uint32_t off, uint32_t *r) {
 __device__ __forceinline__ uint32_t zero_pair(uint32_t z) {
     const __nv_bfloat162 p = __float2bfloat162_rn(static_cast<float>(z) * (-1.f / 64.f));   // exact
     return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+__device__ __forceinline__ float ld_scale(const HeadArgs &a, long long at) {
+    return a.scale_f32 ? __ldg(static_cast<const float *>(a.scale) + at)
+                       : ld_elem<2>(static_cast<const char *>(a.scale), at);
 }
 
 // Codes of every stage (one lane).  start() asks for the first tile's before
@@ -466,30 +463,26 @@ __device__ bool mma_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBa
             break;
         }
 #pragma unroll 1
-        for (int j = 0; j < Cfg::kBatches; ++j, ++i) {
+        for (int j = 0; j < Cfg::kSubs; ++j, ++i) {
             const uint32_t d = i % Cfg::DB;
             const uint32_t parity = ((i / Cfg::DB) & 1) ^ 1;
             if (!warp_wait(&bar.dempty[d], parity) ||
-                (halves == 2 && !warp_wait(&bar.dempty[(Cfg::AW - 1) * Cfg::DB + d], parity))) { ok = false; break; }
+                (halves == 2 && !warp_wait(&bar.dempty[Cfg::DB + d], parity))) { ok = false; break; }
             tc_fence_after();
-            const int live = min(Cfg::GB, subs - j * Cfg::GB);   // groups of the batch
 #pragma unroll 1
             for (int h = 0; h < halves; ++h) {
-                uint32_t acc = tmem + (h * Cfg::DB + d) * Cfg::GB * NH;
-                const uint32_t xh = xs + h * (Cfg::AK / 64) * nh8;
-#pragma unroll
-                for (int g = 0; g < Cfg::GB; ++g, acc += NH) {
-                    if (g >= live) break;
+                const uint32_t acc = tmem + (h * Cfg::DB + d) * NH, xh = xs + h * (Cfg::AK / 64) * nh8;
+                if (j < subs) {
 #pragma unroll
                     for (int w = 0; w < GROUP / kUnit; ++w) {
-                        const int k = k32 + (g * GROUP + w * kUnit) / 32;   // 32-k block of the stage
+                        const int k = k32 + w * kUnit / 32;   // 32-k block of the stage
                         mma_ts<kUnit>(acc, acol + 16 * (k - k32), xh + (k >> 1) * nh8 + (k & 1) * 4, idesc, w > 0);
                     }
                 }
                 mma_commit(&bar.dfull[h * Cfg::DB + d]);
             }
-            acol += Cfg::GB * GROUP / 2;
-            k32 += Cfg::GB * GROUP / 32;
+            acol += GROUP / 2;
+            k32 += GROUP / 32;
         }
         if (!ok) break;
         mma_commit(&bar.done[s % kDone]);
@@ -548,8 +541,7 @@ __device__ bool param_role(const HeadArgs &a, const TokenPlan &t, int jobs, Head
                     for (int q = 0; q < kParGroups; ++q) {
                         const long long e = at[r] + min(q, a.G - 1 - g0);
                         p.scale[q][r * 32 + lane] =
-                            64.f * (a.scale_f32 ? __ldg(static_cast<const float *>(a.scale) + e)
-                                                : ld_elem<2>(static_cast<const char *>(a.scale), e));
+                            64.f * ld_scale(a, e);
                         if (a.zero) p.off[q][r * 32 + lane] = zero_pair(__ldg(a.zero + e) & 15u);
                     }
                 }
@@ -660,7 +652,7 @@ __device__ bool accumulate_role(const HeadArgs &a, const TokenPlan &t, int jobs,
                                 const ParChunk *par, uint32_t tmem, int h) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarter = warp & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    int i = 0, c = 0;
+    int i = 0, slot = 0, phase = 0;       // batch; slot and phase of the parameter ring
     for (int job = 0; job < jobs; ++job) {
         const int tile = blockIdx.x + job / t.passes * gridDim.x, pass = job % t.passes;
         const int v = tile * kTileV + quarter * 32 + lane;
@@ -676,54 +668,41 @@ __device__ bool accumulate_role(const HeadArgs &a, const TokenPlan &t, int jobs,
 #pragma unroll 1
         for (int kb = 0; kb < a.nkb; ++kb) {
 #pragma unroll 1
-            for (int j = 0; j < Cfg::kBatches; ++j, ++i) {
-                const int gi = kb * Cfg::kSubs + j * Cfg::GB, db = h * Cfg::DB + i % Cfg::DB;
-                const int slot = c % kParSlots;
-                if (gi % kParGroups == 0 && gi < a.G && !warp_wait(&bar.pfull[slot], (c / kParSlots) & 1)) return false;
+            for (int j = 0; j < Cfg::kSubs; ++j, ++i) {
+                const int g = kb * Cfg::kSubs + j, db = h * Cfg::DB + i % Cfg::DB;
+                if (g % kParGroups == 0 && g < a.G && !warp_wait(&bar.pfull[slot], phase)) return false;
                 if (!warp_wait(&bar.dfull[db], (i / Cfg::DB) & 1)) return false;
                 tc_fence_after();
-                if (gi < a.G) {
-                    const float *scale = &par[slot].scale[gi % kParGroups][quarter * 32 + lane];
-                    const uint32_t src = lanes + db * Cfg::GB * NH;
-                    // Blocks of kLoad columns, groups outside; the next block
-                    // is on its way while one is added.
-                    constexpr int kBlocks = NH / Cfg::kLoad;
+                if (g < a.G) {
+                    const float sc = par[slot].scale[g % kParGroups][quarter * 32 + lane];
+                    const float2 ss = make_float2(sc, sc);
+                    const uint32_t src = lanes + db * NH;
+                    // The next columns are on their way while these are added.
                     float d[2][Cfg::kLoad];
                     tmem_ld(src, d[0]);
 #pragma unroll
-                    for (int q = 0; q < Cfg::GB; ++q) {
-                        if (Cfg::GB > 1 && gi + q >= a.G) break;
-                        const float sc = scale[q * kTileV];
-                        const float2 ss = make_float2(sc, sc);
+                    for (int k = 0; k < NH / Cfg::kLoad; ++k) {
+                        if (Cfg::kLoad * k < t.nh) {
+                            tc_wait_ld(d[k & 1]);
+                            if (k + 1 < NH / Cfg::kLoad && Cfg::kLoad * (k + 1) < t.nh)
+                                tmem_ld(src + Cfg::kLoad * (k + 1), d[(k + 1) & 1]);
 #pragma unroll
-                        for (int k = 0; k < kBlocks; ++k) {
-                            if (Cfg::kLoad * k < t.nh) {
-                                const int at = q * kBlocks + k;
-                                tc_wait_ld(d[at & 1]);
-                                if (k + 1 < kBlocks && Cfg::kLoad * (k + 1) < t.nh)
-                                    tmem_ld(src + q * NH + Cfg::kLoad * (k + 1), d[(at + 1) & 1]);
-                                else if (kBlocks == 1 && q + 1 < Cfg::GB)
-                                    tmem_ld(src + (q + 1) * NH, d[(at + 1) & 1]);
-#pragma unroll
-                                for (int n = 0; n < Cfg::kLoad; n += 2) {
-                                    float *y = acc + Cfg::kLoad * k + n;
-                                    const float2 z = __ffma2_rn(make_float2(d[at & 1][n], d[at & 1][n + 1]), ss,
-                                                                make_float2(y[0], y[1]));
-                                    y[0] = z.x;
-                                    y[1] = z.y;
-                                }
+                            for (int n = 0; n < Cfg::kLoad; n += 2) {
+                                float *y = acc + Cfg::kLoad * k + n;
+                                const float2 z = __ffma2_rn(make_float2(d[k & 1][n], d[k & 1][n + 1]), ss,
+                                                            make_float2(y[0], y[1]));
+                                y[0] = z.x;
+                                y[1] = z.y;
                             }
                         }
                     }
-                    // A group's last load may still be in flight (of a group past the end).
-                    tc_wait_ld(d[0]);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.dempty[db]);
-                if (gi < a.G && ((gi + Cfg::GB) % kParGroups == 0 || gi + Cfg::GB >= a.G)) {
+                if (g < a.G && ((g + 1) % kParGroups == 0 || g + 1 == a.G)) {
                     if (lane == 0) mbar_arrive(&bar.pempty[slot]);
-                    ++c;
+                    if (++slot == kParSlots) { slot = 0; phase ^= 1; }
                 }
             }
         }
@@ -764,7 +743,7 @@ head_kernel(HeadArgs a, const __grid_constant__ CUtensorMap map) {
         for (int i = 0; i < Cfg::XS; ++i) mbar_init(&bar.xfull[i], 1);
         for (int i = 0; i < Cfg::AS; ++i) mbar_init(&bar.afull[i], 4);
         for (int i = 0; i < kDone; ++i) mbar_init(&bar.done[i], 1);
-        for (int i = 0; i < Cfg::AW * Cfg::DB; ++i) { mbar_init(&bar.dfull[i], 1); mbar_init(&bar.dempty[i], 4); }
+        for (int i = 0; i < 2 * Cfg::DB; ++i) { mbar_init(&bar.dfull[i], 1); mbar_init(&bar.dempty[i], 4); }
         fence_mbar_init();
         // The codes of the first stages are asked for at once: the pack
         // kernel let this grid launch after its own wait, so whatever ran
@@ -791,7 +770,7 @@ head_kernel(HeadArgs a, const __grid_constant__ CUtensorMap map) {
     const int jobs = my_tiles * t.passes;
     bool ok = true;
     if (wg == 0) {
-        if constexpr (Cfg::kSplit) regs_less<Cfg::kRegs0>();
+        regs_less<Cfg::kRegs0>();
         if (warp == 0) {
             if (lane == 0) ok = codes.run(t, jobs);
         } else if (warp == 1) {
@@ -802,10 +781,10 @@ head_kernel(HeadArgs a, const __grid_constant__ CUtensorMap map) {
             ok = param_role(a, t, jobs, bar, par);
         }
     } else if (wg <= Cfg::WW) {
-        if constexpr (Cfg::kSplit) regs_less<Cfg::kRegsW>();
+        regs_less<Cfg::kRegsW>();
         ok = widen_role<Cfg, GROUP>(a, t, jobs, bar, cring, par, tmem, wg - 1);
     } else {
-        if constexpr (Cfg::kSplit) regs_more<Cfg::kRegsA>();
+        regs_more<Cfg::kRegsA>();
         const int h = wg - 1 - Cfg::WW;
         if (h < t.halves) ok = accumulate_role<Cfg, NH>(a, t, jobs, bar, par, tmem, h);
     }
@@ -815,6 +794,273 @@ head_kernel(HeadArgs a, const __grid_constant__ CUtensorMap map) {
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_free(tmem, kTmemCols);
+}
+
+// ---------------------------------------------------------------------------
+// 4. Few tokens: one launch, no tensor memory.
+//
+// With at most 16 tokens nothing but the weights' bytes costs, and the
+// hand-overs between roles above would set the pace (measured at one token of
+// 129280 x 4096: 78 us).  Here a warp does all of it for 16 vocabulary rows:
+// codes straight into registers, up to four blocks of 128 k ahead; widened there;
+// multiplied by mma.sync with the rows as M = 16 and the tokens as N = 8 or 16
+// (the matrix unit is idle most of the time, so its older path is enough);
+// group sums scaled and added in fp32.  Of rows g and g + 8 (g = lane / 4) lane
+// t = lane % 4 of a quad reads the t-th quarter of every group, and its codes
+// take the places of the k that the instruction expects in that lane; x
+// stands in shared memory in the same order, so nothing is shuffled.  `split`
+// warps share a tile's k and add their sums in a fixed order.
+// ---------------------------------------------------------------------------
+constexpr int kFewThreads = 512;
+constexpr int kFewTokens = 16;
+constexpr size_t kFewSmem = 190 * 1024;  // x at most
+
+// Bytes of one token of x: its 128-k blocks, and 64 more if needed so that two
+// neighbouring tokens lie in different halves of the banks.
+__host__ __device__ __forceinline__ int few_pitch(int H) { return (H + 127) / 128 * 256 + 64; }
+static size_t few_smem(int M, int H) { return static_cast<size_t>(M) * few_pitch(H); }
+
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A lane's codes of one group: kWords words, zero if the group is past the end.
+// Groups of 32 and 64 leave part of a 32-byte sector to the next load, which
+// finds it in L1.
+template <int WORDS> __device__ __forceinline__ void ld_codes(uint32_t *w, const uint8_t *p, bool in) {
+    if (WORDS == 4) {
+        const uint4 u = in ? ld_stream(p) : make_uint4(0, 0, 0, 0);
+        w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+    } else if (WORDS == 2) {
+        const uint2 u = in ? __ldg(reinterpret_cast<const uint2 *>(p)) : make_uint2(0, 0);
+        w[0] = u.x; w[1] = u.y;
+    } else {
+        w[0] = in ? __ldg(reinterpret_cast<const uint32_t *>(p)) : 0u;
+    }
+}
+
+// NT: token tiles of 8.  ZERO: the weights have zero points.
+template <int NT, int GROUP, bool ZERO>
+__global__ void __launch_bounds__(kFewThreads, 1) few_kernel(HeadArgs a, int split) {
+    constexpr int kSubs = 128 / GROUP, kWords = GROUP / 32, kWarps = kFewThreads / 32;
+    constexpr int kBlocks = GROUP == 128 ? 2 : 1;          // blocks of 128 k in a step
+    constexpr int kAhead = GROUP == 64 ? 3 : 2;            // steps on their way
+    extern __shared__ __align__(16) char dyn[];
+    __shared__ float sums[2][kWarps][NT * 4][32];
+    __shared__ int rows[kFewTokens];
+    __shared__ int s_count;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    griddep_wait();
+    griddep_launch_dependents();
+    if (tid == 0) {
+        int n = 0;
+        for (int b = 0; b < a.B; ++b)
+            for (int p = 0, np = row_positions(a, b); p < np; ++p) rows[n++] = b * a.P + p;
+        s_count = n;
+    }
+    __syncthreads();
+    const int count = s_count, pitch = few_pitch(a.H), nkb = (a.H + 127) / 128;
+    if (count == 0) return;
+    // x: chunk (block kb, word w, lane t) of a token at 16 kb + 4 w + t, its eight
+    // values in the order 0 4 1 5 2 6 3 7 (see widen8).
+    const int per = nkb * 16;
+    for (int i = tid; i < count * per; i += kFewThreads) {
+        const int tok = i / per, c = i - tok * per;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (c * 8 < a.H) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(a.x + static_cast<long long>(rows[tok]) * a.H) + c);
+            w.x = __byte_perm(u.x, u.z, 0x5410);
+            w.y = __byte_perm(u.x, u.z, 0x7632);
+            w.z = __byte_perm(u.y, u.w, 0x5410);
+            w.w = __byte_perm(u.y, u.w, 0x7632);
+        }
+        constexpr int kIn = GROUP / 8;    // chunks of a group: kWords for each lane of a quad
+        const int q = (c & 15) / kIn, ct = (c & 15) % kIn / kWords, cw = (c & 15) % kWords;
+        *reinterpret_cast<uint4 *>(dyn + tok * pitch + ((c & ~15) + (q * kWords + cw) * 4 + ct) * 16) = w;
+    }
+    __syncthreads();
+
+    // This warp's blocks of a tile's k, and its tiles: the steps of all of
+    // them are one sequence, so the loads run ahead across tiles too.
+    const int share = warp % split, lo = nkb * share / split, hi = nkb * (share + 1) / split;
+    const int tiles = (a.V + 15) / 16, stride = gridDim.x * (kWarps / split);
+    const int first = blockIdx.x * (kWarps / split) + warp / split;
+    const long long row_bytes = a.H / 2;
+    const char *xb[NT];                   // this lane's tokens and place; columns past the last token are not used
+#pragma unroll
+    for (int n = 0; n < NT; ++n) xb[n] = dyn + min(8 * n + g, count - 1) * pitch + t * 16;
+    const int es = a.scale_f32 ? 4 : 2;
+
+    uint32_t w[kAhead][kBlocks][2][4];    // codes, scales and zero points on their way
+    uint32_t sc[kAhead][kBlocks][2][kSubs], zp[kAhead][kBlocks][2][kSubs];
+    const uint8_t *codes[2], *zero[2];    // next block to fetch
+    const char *scale[2];
+    int f_tile = first, f_kb = lo;
+    auto aim = [&]() {                    // rows g and g + 8 (past the end: the last row again)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const long long v = min(f_tile * 16 + g + 8 * r, a.V - 1);
+            codes[r] = a.codes + v * row_bytes + lo * 64 + t * (GROUP / 8);
+            scale[r] = static_cast<const char *>(a.scale) + (v * a.G + lo * kSubs) * es;
+            if (ZERO) zero[r] = a.zero + v * a.G + lo * kSubs;
+        }
+    };
+    auto fetch = [&](int u) {
+        if (f_tile >= tiles) return;
+#pragma unroll
+        for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+            for (int q = 0; q < kSubs; ++q) {
+                const bool in = f_kb + k < hi && (f_kb + k) * kSubs + q < a.G;
+                const int at = k * kSubs + q;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    ld_codes<kWords>(w[u][k][r] + q * kWords, codes[r] + at * (GROUP / 2), in);
+                    if (in) {
+                        sc[u][k][r][q] = a.scale_f32 ? __ldg(reinterpret_cast<const uint32_t *>(scale[r]) + at)
+                                                     : __ldg(reinterpret_cast<const unsigned short *>(scale[r]) + at);
+                        if (ZERO) zp[u][k][r][q] = __ldg(zero[r] + at);
+                    }
+                }
+            }
+        f_kb += kBlocks;
+        if (f_kb < hi) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                codes[r] += kBlocks * 64;
+                scale[r] += kBlocks * kSubs * es;
+                if (ZERO) zero[r] += kBlocks * kSubs;
+            }
+        } else {
+            f_kb = lo;
+            f_tile += stride;
+            aim();
+        }
+    };
+    float acc[NT][4];
+    auto clear = [&]() {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+    };
+    // The split's sums of a finished tile.  Two sets in turn: a warp that
+    // writes a set has passed the barrier after which its readers were done.
+    int turn = 0;
+    auto finish = [&](int tile) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sums[turn][warp][4 * n + i][lane] = acc[n][i];
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / split), "r"(32 * split) : "memory");
+        for (int i = share; i < 4 * NT; i += split) {
+            float y = 0.f;
+            for (int j = 0; j < split; ++j) y += sums[turn][warp - share + j][i][lane];
+            y *= 64.f;                    // widen8 gives code / 64
+            const int tok = i / 4 * 8 + 2 * t + (i & 1), v = tile * 16 + g + (i & 2) * 4;
+            if (tok < count && v < a.V) {
+                const long long o = static_cast<long long>(rows[tok]) * a.V + v;
+                if (a.out_f32) store_logit(static_cast<float *>(a.out) + o, y);
+                else store_logit(static_cast<__nv_bfloat16 *>(a.out) + o, y);
+            }
+        }
+        turn ^= 1;
+        clear();
+    };
+    clear();
+    if (lo == hi) {                       // more warps than blocks: nothing to add
+        for (int tile = first; tile < tiles; tile += stride) finish(tile);
+        return;
+    }
+    aim();
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) fetch(u);
+    const uint32_t eight = zero_pair(8);
+    int tile = first, kb = lo;
+    while (tile < tiles) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+#pragma unroll
+            for (int k = 0; k < kBlocks; ++k) {
+                if (k > 0 && kb + k >= hi) break;
+                const int xk = (kb + k) * 256;
+#pragma unroll
+                for (int q = 0; q < kSubs; ++q) {
+                    if (kSubs > 1 && (kb + k) * kSubs + q >= a.G) break;
+                    float part[NT][4];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) part[n][i] = 0.f;
+                    const uint32_t o0 = ZERO ? zero_pair(zp[u][k][0][q] & 15u) : eight;
+                    const uint32_t o1 = ZERO ? zero_pair(zp[u][k][1][q] & 15u) : eight;
+#pragma unroll
+                    for (int i = 0; i < kWords; ++i) {
+                        uint32_t r0[4], r1[4];
+                        widen8(w[u][k][0][q * kWords + i], o0, r0);
+                        widen8(w[u][k][1][q * kWords + i], o1, r1);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const uint4 b = *reinterpret_cast<const uint4 *>(xb[n] + xk + (q * kWords + i) * 64);
+                            mma_16x8x16(part[n], r0[0], r1[0], r0[1], r1[1], b.x, b.y);
+                            mma_16x8x16(part[n], r0[2], r1[2], r0[3], r1[3], b.z, b.w);
+                        }
+                    }
+                    const float f0 = __uint_as_float(a.scale_f32 ? sc[u][k][0][q] : sc[u][k][0][q] << 16);
+                    const float f1 = __uint_as_float(a.scale_f32 ? sc[u][k][1][q] : sc[u][k][1][q] << 16);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        acc[n][0] = fmaf(f0, part[n][0], acc[n][0]);
+                        acc[n][1] = fmaf(f0, part[n][1], acc[n][1]);
+                        acc[n][2] = fmaf(f1, part[n][2], acc[n][2]);
+                        acc[n][3] = fmaf(f1, part[n][3], acc[n][3]);
+                    }
+                }
+            }
+            fetch(u);
+            kb += kBlocks;
+            if (kb >= hi) {
+                finish(tile);
+                kb = lo;
+                tile += stride;
+                if (tile >= tiles) break;
+            }
+        }
+    }
+}
+
+template <int NT, int GROUP, bool ZERO> static cudaError_t launch_few(const HeadArgs &a, int M, cudaStream_t st) {
+    static std::atomic<bool> attr_set[64];
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && !attr_set[dev & 63].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(few_kernel<NT, GROUP, ZERO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(kFewSmem));
+        if (e == cudaSuccess) attr_set[dev & 63].store(true, std::memory_order_release);
+    }
+    if (e != cudaSuccess) return e;
+    // Two warps to a tile keep the last round of tiles short; sixteen where
+    // there are too few tiles to occupy the SMs otherwise.
+    const int tiles = (a.V + 15) / 16, split = tiles <= 4 * sms ? 16 : 2;
+    const int per = kFewThreads / 32 / split, need = (tiles + per - 1) / per;
+    return launch_pdl(few_kernel<NT, GROUP, ZERO>, dim3(need < sms ? need : sms), dim3(kFewThreads), few_smem(M, a.H), st,
+                      a, split);
+}
+
+template <int NT, bool ZERO> static cudaError_t launch_few_group(const HeadArgs &a, int M, cudaStream_t st) {
+    if (a.group == 128) return launch_few<NT, 128, ZERO>(a, M, st);
+    if (a.group == 64) return launch_few<NT, 64, ZERO>(a, M, st);
+    return launch_few<NT, 32, ZERO>(a, M, st);
+}
+
+static cudaError_t launch_few_tokens(const HeadArgs &a, int M, cudaStream_t st) {
+    if (M <= 8) return a.zero ? launch_few_group<1, true>(a, M, st) : launch_few_group<1, false>(a, M, st);
+    return a.zero ? launch_few_group<2, true>(a, M, st) : launch_few_group<2, false>(a, M, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -831,8 +1077,10 @@ static sv_status head_check(const sv_w4 *w, int B, int P) {
 }
 
 // Tokens per half for a batch of at most M tokens, and k per stage.
-static int nh_for(int M) { return M <= 16 ? 16 : M <= 128 ? 64 : 96; }
+static int nh_for(int M) { return M <= 128 ? 64 : 96; }
 static int ak_for(int nh) { return nh <= 64 ? 256 : 128; }
+
+static bool few(const sv_w4 *w, int M) { return M <= kFewTokens && few_smem(M, w->H) <= kFewSmem; }
 
 struct HeadPlan {
     size_t off_rows, off_image, bytes;
@@ -846,7 +1094,7 @@ static HeadPlan head_plan(const sv_w4 *w, int B, int P) {
     p.off_image = align(16 + 4ull * M);
     // Whatever the scheduled count is, it packs into at most as many passes
     // as M does, each of at most 2 nh tokens.
-    const size_t most = nh == 16 ? 16 : 2 * nh, passes = (M + most - 1) / most;
+    const size_t most = 2 * nh, passes = (M + most - 1) / most;
     p.bytes = p.off_image + passes * most * nkb * ak * 2ull;
     return p;
 }
@@ -903,7 +1151,7 @@ template <int NH> static cudaError_t launch_group(const HeadArgs &a, const CUten
 }  // namespace sv
 
 extern "C" size_t sv_head_w4_workspace_bytes(const sv_w4 *weight, int B, int P) {
-    if (sv::head_check(weight, B, P) != SV_OK || B == 0) return 0;
+    if (sv::head_check(weight, B, P) != SV_OK || B == 0 || sv::few(weight, B * P)) return 0;
     return sv::head_plan(weight, B, P).bytes;
 }
 
@@ -915,14 +1163,16 @@ extern "C" sv_status sv_head_w4(const sv_w4 *weight, const void *x, int B, int P
     if (const sv_status e = sv::head_check(weight, B, P)) return e;
     if (out_dtype != SV_F32 && out_dtype != SV_BF16) return SV_ERR_DTYPE;
     if (B == 0) return SV_OK;
-    if (!weight->codes || !weight->scale || !x || !out || !workspace) return SV_ERR_ARG;
+    if (!weight->codes || !weight->scale || !x || !out) return SV_ERR_ARG;
     if ((reinterpret_cast<uintptr_t>(weight->codes) | reinterpret_cast<uintptr_t>(x) |
          reinterpret_cast<uintptr_t>(workspace)) & 15)
         return SV_ERR_ARG;
     if (reinterpret_cast<uintptr_t>(weight->scale) & (weight->scale_dtype == SV_F32 ? 3 : 1)) return SV_ERR_ARG;
     if (reinterpret_cast<uintptr_t>(out) & (out_dtype == SV_F32 ? 3 : 1)) return SV_ERR_ARG;
+    const bool few = sv::few(weight, B * P);
+    if (!few && !workspace) return SV_ERR_ARG;
     const sv::HeadPlan p = sv::head_plan(weight, B, P);
-    if (workspace_bytes < p.bytes) return SV_ERR_WORKSPACE;
+    if (!few && workspace_bytes < p.bytes) return SV_ERR_WORKSPACE;
     sv::HeadArgs a = {};
     a.codes = weight->codes; a.scale = weight->scale; a.zero = weight->zero;
     a.scale_f32 = weight->scale_dtype == SV_F32;
@@ -932,6 +1182,8 @@ extern "C" sv_status sv_head_w4(const sv_w4 *weight, const void *x, int B, int P
     a.x = static_cast<const __nv_bfloat16 *>(x);
     a.B = B; a.P = P; a.lengths = lengths; a.extra = extra; a.out = out;
     const int M = B * P;
+    if (few)
+        return sv::note_cuda(sv::launch_few_tokens(a, M, static_cast<cudaStream_t>(stream)));
     a.nh_max = sv::nh_for(M);
     a.ak = sv::ak_for(a.nh_max);
     a.nkb = (a.H + a.ak - 1) / a.ak;
@@ -948,7 +1200,6 @@ extern "C" sv_status sv_head_w4(const sv_w4 *weight, const void *x, int B, int P
     e = sv::launch_pdl(sv::pack_kernel, dim3(packs), dim3(sv::kPackThreads), 0, st, a);
     if (e != cudaSuccess) return sv::note_cuda(e);
     switch (a.nh_max) {
-    case 16: e = sv::launch_group<16>(a, map, st); break;
     case 64: e = sv::launch_group<64>(a, map, st); break;
     default: e = sv::launch_group<96>(a, map, st); break;
     }

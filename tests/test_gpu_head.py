@@ -38,12 +38,11 @@ class Head:
         buf = torch.full((n + 2 * pad,), 55.0, dtype=DT[dtype], device="cuda")
         out = buf[pad + 1:pad + 1 + n].view(B, P, self.V)      # no 16-byte boundary
         need = sv.sv_head_w4_workspace_bytes(self.weight, B, P)
-        assert need > 0
         ws = torch.full((need + 16,), 255, dtype=torch.uint8, device="cuda")
         st = torch.zeros(1, dtype=torch.int32, device="cuda")
         torch.cuda.synchronize()
-        sv.sv_head_w4(self.weight, x, out, ws[:need], lengths=lengths, extra=extra, status=st,
-                      stream=stream)
+        sv.sv_head_w4(self.weight, x, out, ws[:need] if need else None, lengths=lengths,
+                      extra=extra, status=st, stream=stream)
         torch.cuda.synchronize()
         assert bool((buf[:pad + 1] == 55).all() and (buf[pad + 1 + n:] == 55).all())
         assert bool((ws[need:] == 255).all()) and int(st) == 0
@@ -70,7 +69,7 @@ SHAPES = [(32, 1, 32), (64, 7, 32), (64, 8, 64), (128, 33, 128), (96, 100, 32), 
 @pytest.mark.parametrize("zero,scale", [(False, "bfloat16"), (True, "float32")])
 def test_head(H, V, group, zero, scale):
     h = Head(H, V, group, zero, scale, seed=H + V)
-    for B, P in ((1, 1), (1, 2), (3, 1), (1, 5), (1, 8), (3, 3), (2, 8), (17, 1)):
+    for B, P in ((1, 1), (1, 2), (3, 1), (1, 5), (1, 8), (3, 3), (2, 8), (1, 9), (17, 1)):
         for dtype in ("float32", "bfloat16"):
             h.check(h.x(B, P), dtype)
 
@@ -85,7 +84,21 @@ def test_head_many_tokens(M, H, V, group, zero):
         h.check(h.x(M, 1), dtype)
 
 
-@pytest.mark.parametrize("B,P", [(1, 1), (5, 4), (40, 5), (3, 9)])
+@pytest.mark.parametrize("H,M", [(16384, 1), (16384, 9), (32768, 1), (32768, 3), (12160, 8), (12288, 16)])
+def test_head_long_rows(H, M):
+    h = Head(H, 150, 64, True, "bfloat16", seed=H + M)
+    for dtype in ("float32", "bfloat16"):
+        h.check(h.x(M, 1), dtype)
+
+
+@pytest.mark.parametrize("V", [16 * 4 * 148, 16 * 4 * 148 + 1, 40000])
+def test_head_few_tokens_of_a_large_vocabulary(V):
+    h = Head(160, V, 32, True, "bfloat16", seed=V)
+    for M in (1, 8, 16):
+        h.check(h.x(M, 1), "float32")
+
+
+@pytest.mark.parametrize("B,P", [(1, 1), (5, 4), (40, 5), (3, 9), (16, 1)])
 def test_head_leaves_unscheduled_positions_as_they_were(B, P):
     h = Head(512, 1031, 128, True, "bfloat16", seed=B)
     for extra in (0, 1):
@@ -154,6 +167,8 @@ def test_head_refuses_a_short_workspace():
     h = Head(4096, 1000, 128, False, "bfloat16", seed=1)
     for M in (1, 100):
         need = sv.sv_head_w4_workspace_bytes(h.weight, M, 1)
+        if need == 0:
+            continue
         x, out = h.x(M, 1), torch.zeros(M, 1, 1000, device="cuda")
         with pytest.raises(sv.SVError) as e:
             sv.sv_head_w4(h.weight, x, out, torch.empty(need - 1, dtype=torch.uint8, device="cuda"))

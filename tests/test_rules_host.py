@@ -108,7 +108,7 @@ def _head(weight=None, **kw):
     (dict(codes=A[0] + 8), ARG), (dict(x=A[1] + 2), ARG), (dict(scale=A[4] + 1), ARG),
     (dict(scale_dtype=sv.SV_F32, scale=A[4] + 2), ARG), (dict(out=A[2] + 1), ARG),
     (dict(out_dtype=sv.SV_F32, out=A[2] + 2), ARG), (dict(ws=A[3] + 8), ARG),
-    (dict(ws=None), ARG), (dict(wsb=1000), WORKSPACE),
+    (dict(ws=None, B=20), ARG), (dict(wsb=1000, B=20), WORKSPACE),
     (dict(out_dtype=2), DTYPE), (dict(scale_dtype=7), DTYPE),
     (dict(V=0), SHAPE), (dict(V=(1 << 20) + 1), SHAPE), (dict(H=0), SHAPE), (dict(H=96), SHAPE),
     (dict(group=16), SHAPE), (dict(group=256), SHAPE), (dict(H=32768 + 64), SHAPE),
