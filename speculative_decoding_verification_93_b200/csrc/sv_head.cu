@@ -801,24 +801,28 @@ head_kernel(HeadArgs a, const __grid_constant__ CUtensorMap map) {
 //
 // With at most 16 tokens nothing but the weights' bytes costs, and the
 // hand-overs between roles above would set the pace (measured at one token of
-// 129280 x 4096: 78 us).  Here a warp does all of it for 16 vocabulary rows:
-// codes straight into registers, up to four blocks of 128 k ahead; widened there;
+// 129280 x 4096: 78 us).  Here a warp does all of it for 32 vocabulary rows:
+// codes straight into registers, two blocks of 128 k ahead; widened there;
 // multiplied by mma.sync with the rows as M = 16 and the tokens as N = 8 or 16
 // (the matrix unit is idle most of the time, so its older path is enough);
-// group sums scaled and added in fp32.  Of rows g and g + 8 (g = lane / 4) lane
-// t = lane % 4 of a quad reads the t-th quarter of every group, and its codes
+// group sums scaled and added in fp32.  Of rows g + 8 r (g = lane / 4) lane t =
+// lane % 4 of a quad reads the t-th quarter of every group, and its codes
 // take the places of the k that the instruction expects in that lane; x
 // stands in shared memory in the same order, so nothing is shuffled.  `split`
 // warps share a tile's k and add their sums in a fixed order.
 // ---------------------------------------------------------------------------
 constexpr int kFewThreads = 512;
 constexpr int kFewTokens = 16;
-constexpr size_t kFewSmem = 190 * 1024;  // x at most
+constexpr int kFewRows = 32;             // rows of a tile: two M = 16 that share every read of x
+constexpr size_t kFewSmem = 224 * 1024;  // x and the split's sums at most
 
 // Bytes of one token of x: its 128-k blocks, and 64 more if needed so that two
 // neighbouring tokens lie in different halves of the banks.
 __host__ __device__ __forceinline__ int few_pitch(int H) { return (H + 127) / 128 * 256 + 64; }
-static size_t few_smem(int M, int H) { return static_cast<size_t>(M) * few_pitch(H); }
+static size_t few_smem(int M, int H) {   // x, then two sets of sums
+    const int NT = (M + 7) / 8;
+    return static_cast<size_t>(M) * few_pitch(H) + sizeof(float) * 2 * kFewThreads * NT * 8;
+}
 
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                             uint32_t b0, uint32_t b1) {
@@ -828,18 +832,17 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A lane's codes of one group: kWords words, zero if the group is past the end.
-// Groups of 32 and 64 leave part of a 32-byte sector to the next load, which
-// finds it in L1.
-template <int WORDS> __device__ __forceinline__ void ld_codes(uint32_t *w, const uint8_t *p, bool in) {
+// A lane's codes of one group: kWords words.  Groups of 32 and 64 leave part of
+// a 32-byte sector to the next load, which finds it in L1.
+template <int WORDS> __device__ __forceinline__ void ld_codes(uint32_t *w, const uint8_t *p) {
     if (WORDS == 4) {
-        const uint4 u = in ? ld_stream(p) : make_uint4(0, 0, 0, 0);
+        const uint4 u = ld_stream(p);
         w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
     } else if (WORDS == 2) {
-        const uint2 u = in ? __ldg(reinterpret_cast<const uint2 *>(p)) : make_uint2(0, 0);
+        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
         w[0] = u.x; w[1] = u.y;
     } else {
-        w[0] = in ? __ldg(reinterpret_cast<const uint32_t *>(p)) : 0u;
+        w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
     }
 }
 
@@ -847,10 +850,9 @@ template <int WORDS> __device__ __forceinline__ void ld_codes(uint32_t *w, const
 template <int NT, int GROUP, bool ZERO>
 __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(HeadArgs a, int split) {
     constexpr int kSubs = 128 / GROUP, kWords = GROUP / 32, kWarps = kFewThreads / 32;
-    constexpr int kBlocks = GROUP == 128 ? 2 : 1;          // blocks of 128 k in a step
-    constexpr int kAhead = GROUP == 64 ? 3 : 2;            // steps on their way
+    constexpr int kAhead = 2;             // blocks on their way
+    constexpr int kSet = GROUP == 32 ? kAhead : 2;   // scale sets: one a block, or the current and the next
     extern __shared__ __align__(16) char dyn[];
-    __shared__ float sums[2][kWarps][NT * 4][32];
     __shared__ int rows[kFewTokens];
     __shared__ int s_count;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -865,104 +867,104 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(HeadArgs a, int spl
     __syncthreads();
     const int count = s_count, pitch = few_pitch(a.H), nkb = (a.H + 127) / 128;
     if (count == 0) return;
+    float(*sums)[kWarps][NT * 8][32] = reinterpret_cast<float(*)[kWarps][NT * 8][32]>(dyn + a.B * a.P * pitch);
     // x: chunk (block kb, word w, lane t) of a token at 16 kb + 4 w + t, its eight
     // values in the order 0 4 1 5 2 6 3 7 (see widen8).
     const int per = nkb * 16;
     for (int i = tid; i < count * per; i += kFewThreads) {
         const int tok = i / per, c = i - tok * per;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (c * 8 < a.H) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(a.x + static_cast<long long>(rows[tok]) * a.H) + c);
-            w.x = __byte_perm(u.x, u.z, 0x5410);
-            w.y = __byte_perm(u.x, u.z, 0x7632);
-            w.z = __byte_perm(u.y, u.w, 0x5410);
-            w.w = __byte_perm(u.y, u.w, 0x7632);
-        }
+        if (c * 8 >= a.H) continue;
+        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(a.x + static_cast<long long>(rows[tok]) * a.H) + c);
+        uint4 w;
+        w.x = __byte_perm(u.x, u.z, 0x5410);
+        w.y = __byte_perm(u.x, u.z, 0x7632);
+        w.z = __byte_perm(u.y, u.w, 0x5410);
+        w.w = __byte_perm(u.y, u.w, 0x7632);
         constexpr int kIn = GROUP / 8;    // chunks of a group: kWords for each lane of a quad
         const int q = (c & 15) / kIn, ct = (c & 15) % kIn / kWords, cw = (c & 15) % kWords;
         *reinterpret_cast<uint4 *>(dyn + tok * pitch + ((c & ~15) + (q * kWords + cw) * 4 + ct) * 16) = w;
     }
     __syncthreads();
 
-    // This warp's blocks of a tile's k, and its tiles: the steps of all of
+    // This warp's blocks of a tile's k, and its tiles: the blocks of all of
     // them are one sequence, so the loads run ahead across tiles too.
     const int share = warp % split, lo = nkb * share / split, hi = nkb * (share + 1) / split;
-    const int tiles = (a.V + 15) / 16, stride = gridDim.x * (kWarps / split);
+    const int tiles = (a.V + kFewRows - 1) / kFewRows, stride = gridDim.x * (kWarps / split);
     const int first = blockIdx.x * (kWarps / split) + warp / split;
+    // The last tile ends with the last row; rows it shares with the one
+    // before are computed twice, to the same bits.
+    auto tile_row = [&](int tile) { return min(tile * kFewRows, a.V - kFewRows); };
     const long long row_bytes = a.H / 2;
     const char *xb[NT];                   // this lane's tokens and place; columns past the last token are not used
 #pragma unroll
     for (int n = 0; n < NT; ++n) xb[n] = dyn + min(8 * n + g, count - 1) * pitch + t * 16;
-    const int es = a.scale_f32 ? 4 : 2;
 
-    uint32_t w[kAhead][kBlocks][2][4];    // codes, scales and zero points on their way
-    uint32_t sc[kAhead][kBlocks][2][kSubs], zp[kAhead][kBlocks][2][kSubs];
-    const uint8_t *codes[2], *zero[2];    // next block to fetch
-    const char *scale[2];
+    // Rows g + 8 r.  Codes on their way; scales and zero points by sets of four
+    // groups, of which each lane of a quad holds one: the rows' reads touch a
+    // quarter of the lines, and a shuffle hands them on.
+    uint32_t w[kAhead][4][4], sc[kSet][4], zp[kSet][4];
+    const uint8_t *codes = nullptr;       // next block to fetch, row g
+    long long par = 0;                    // index of its first scale, row g
     int f_tile = first, f_kb = lo;
-    auto aim = [&]() {                    // rows g and g + 8 (past the end: the last row again)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const long long v = min(f_tile * 16 + g + 8 * r, a.V - 1);
-            codes[r] = a.codes + v * row_bytes + lo * 64 + t * (GROUP / 8);
-            scale[r] = static_cast<const char *>(a.scale) + (v * a.G + lo * kSubs) * es;
-            if (ZERO) zero[r] = a.zero + v * a.G + lo * kSubs;
-        }
+    auto aim = [&]() {
+        const long long v = tile_row(f_tile) + g;
+        codes = a.codes + v * row_bytes + lo * 64 + t * (GROUP / 8);
+        par = v * a.G + lo * kSubs;
     };
     auto fetch = [&](int u) {
         if (f_tile >= tiles) return;
 #pragma unroll
-        for (int k = 0; k < kBlocks; ++k)
+        for (int q = 0; q < kSubs; ++q) {
+            if (kSubs > 1 && f_kb * kSubs + q >= a.G) break;
 #pragma unroll
-            for (int q = 0; q < kSubs; ++q) {
-                const bool in = f_kb + k < hi && (f_kb + k) * kSubs + q < a.G;
-                const int at = k * kSubs + q;
+            for (int r = 0; r < 4; ++r) ld_codes<kWords>(w[u][r] + q * kWords, codes + r * 8 * row_bytes + q * (GROUP / 2));
+        }
+        if ((f_kb - lo) * kSubs % 4 == 0) {
+            const int set = GROUP == 32 ? u : 1;
+            const int in = min(t, a.G - 1 - f_kb * kSubs);    // past the end: any
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    ld_codes<kWords>(w[u][k][r] + q * kWords, codes[r] + at * (GROUP / 2), in);
-                    if (in) {
-                        sc[u][k][r][q] = a.scale_f32 ? __ldg(reinterpret_cast<const uint32_t *>(scale[r]) + at)
-                                                     : __ldg(reinterpret_cast<const unsigned short *>(scale[r]) + at);
-                        if (ZERO) zp[u][k][r][q] = __ldg(zero[r] + at);
-                    }
-                }
+            for (int r = 0; r < 4; ++r) {
+                const long long at = par + r * 8ll * a.G + in;
+                sc[set][r] = a.scale_f32 ? __ldg(static_cast<const uint32_t *>(a.scale) + at)
+                                         : __ldg(static_cast<const unsigned short *>(a.scale) + at);
+                if (ZERO) zp[set][r] = __ldg(a.zero + at);
             }
-        f_kb += kBlocks;
-        if (f_kb < hi) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                codes[r] += kBlocks * 64;
-                scale[r] += kBlocks * kSubs * es;
-                if (ZERO) zero[r] += kBlocks * kSubs;
-            }
-        } else {
+        }
+        codes += 64;
+        par += kSubs;
+        if (++f_kb == hi) {
             f_kb = lo;
             f_tile += stride;
             aim();
         }
     };
-    float acc[NT][4];
+    float acc[2][NT][4];
     auto clear = [&]() {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
     };
     // The split's sums of a finished tile.  Two sets in turn: a warp that
     // writes a set has passed the barrier after which its readers were done.
     int turn = 0;
     auto finish = [&](int tile) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sums[turn][warp][4 * n + i][lane] = acc[n][i];
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sums[turn][warp][(m * NT + n) * 4 + i][lane] = acc[m][n][i];
         asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / split), "r"(32 * split) : "memory");
-        for (int i = share; i < 4 * NT; i += split) {
+        for (int i = share; i < 8 * NT; i += split) {
             float y = 0.f;
             for (int j = 0; j < split; ++j) y += sums[turn][warp - share + j][i][lane];
             y *= 64.f;                    // widen8 gives code / 64
-            const int tok = i / 4 * 8 + 2 * t + (i & 1), v = tile * 16 + g + (i & 2) * 4;
-            if (tok < count && v < a.V) {
+            const int tok = i / 4 % NT * 8 + 2 * t + (i & 1);
+            const int v = tile_row(tile) + i / (4 * NT) * 16 + g + (i & 2) * 4;
+            if (tok < count) {
                 const long long o = static_cast<long long>(rows[tok]) * a.V + v;
                 if (a.out_f32) store_logit(static_cast<float *>(a.out) + o, y);
                 else store_logit(static_cast<__nv_bfloat16 *>(a.out) + o, y);
@@ -984,46 +986,62 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(HeadArgs a, int spl
     while (tile < tiles) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
+            const int in_set = (kb - lo) * kSubs % 4;     // this block's first group in its set
+            const int set = GROUP == 32 ? u : 0;
+            if (in_set == 0) {
 #pragma unroll
-            for (int k = 0; k < kBlocks; ++k) {
-                if (k > 0 && kb + k >= hi) break;
-                const int xk = (kb + k) * 256;
+                for (int r = 0; r < 4; ++r) {
+                    if (GROUP != 32) sc[0][r] = sc[1][r];
+                    if (!a.scale_f32) sc[set][r] <<= 16;
+                    if (ZERO) zp[set][r] = zero_pair(zp[GROUP == 32 ? u : 1][r] & 15u);
+                }
+            }
+            const int xo = kb * 256;
 #pragma unroll
-                for (int q = 0; q < kSubs; ++q) {
-                    if (kSubs > 1 && (kb + k) * kSubs + q >= a.G) break;
-                    float part[NT][4];
+            for (int q = 0; q < kSubs; ++q) {
+                if (kSubs > 1 && kb * kSubs + q >= a.G) break;
+                const int from = (lane & ~3) + in_set + q;
+                float f[4];
+                uint32_t o[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    f[r] = __uint_as_float(__shfl_sync(0xffffffffu, sc[set][r], from));
+                    o[r] = ZERO ? __shfl_sync(0xffffffffu, zp[set][r], from) : eight;
+                }
+                float part[2][NT][4];
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) part[n][i] = 0.f;
-                    const uint32_t o0 = ZERO ? zero_pair(zp[u][k][0][q] & 15u) : eight;
-                    const uint32_t o1 = ZERO ? zero_pair(zp[u][k][1][q] & 15u) : eight;
+                        for (int i = 0; i < 4; ++i) part[m][n][i] = 0.f;
 #pragma unroll
-                    for (int i = 0; i < kWords; ++i) {
+                for (int i = 0; i < kWords; ++i) {
+                    uint4 b[NT];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        b[n] = *reinterpret_cast<const uint4 *>(xb[n] + xo + (q * kWords + i) * 64);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
                         uint32_t r0[4], r1[4];
-                        widen8(w[u][k][0][q * kWords + i], o0, r0);
-                        widen8(w[u][k][1][q * kWords + i], o1, r1);
+                        widen8(w[u][2 * m][q * kWords + i], o[2 * m], r0);
+                        widen8(w[u][2 * m + 1][q * kWords + i], o[2 * m + 1], r1);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            const uint4 b = *reinterpret_cast<const uint4 *>(xb[n] + xk + (q * kWords + i) * 64);
-                            mma_16x8x16(part[n], r0[0], r1[0], r0[1], r1[1], b.x, b.y);
-                            mma_16x8x16(part[n], r0[2], r1[2], r0[3], r1[3], b.z, b.w);
+                            mma_16x8x16(part[m][n], r0[0], r1[0], r0[1], r1[1], b[n].x, b[n].y);
+                            mma_16x8x16(part[m][n], r0[2], r1[2], r0[3], r1[3], b[n].z, b[n].w);
                         }
                     }
-                    const float f0 = __uint_as_float(a.scale_f32 ? sc[u][k][0][q] : sc[u][k][0][q] << 16);
-                    const float f1 = __uint_as_float(a.scale_f32 ? sc[u][k][1][q] : sc[u][k][1][q] << 16);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        acc[n][0] = fmaf(f0, part[n][0], acc[n][0]);
-                        acc[n][1] = fmaf(f0, part[n][1], acc[n][1]);
-                        acc[n][2] = fmaf(f1, part[n][2], acc[n][2]);
-                        acc[n][3] = fmaf(f1, part[n][3], acc[n][3]);
-                    }
                 }
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[m][n][i] = fmaf(f[2 * m + i / 2], part[m][n][i], acc[m][n][i]);
             }
             fetch(u);
-            kb += kBlocks;
-            if (kb >= hi) {
+            if (++kb == hi) {
                 finish(tile);
                 kb = lo;
                 tile += stride;
@@ -1044,9 +1062,9 @@ template <int NT, int GROUP, bool ZERO> static cudaError_t launch_few(const Head
         if (e == cudaSuccess) attr_set[dev & 63].store(true, std::memory_order_release);
     }
     if (e != cudaSuccess) return e;
-    // Two warps to a tile keep the last round of tiles short; sixteen where
+    // Four warps to a tile keep the last round of tiles short; sixteen where
     // there are too few tiles to occupy the SMs otherwise.
-    const int tiles = (a.V + 15) / 16, split = tiles <= 4 * sms ? 16 : 2;
+    const int tiles = (a.V + kFewRows - 1) / kFewRows, split = tiles <= 4 * sms ? 16 : 4;
     const int per = kFewThreads / 32 / split, need = (tiles + per - 1) / per;
     return launch_pdl(few_kernel<NT, GROUP, ZERO>, dim3(need < sms ? need : sms), dim3(kFewThreads), few_smem(M, a.H), st,
                       a, split);
@@ -1080,7 +1098,9 @@ static sv_status head_check(const sv_w4 *w, int B, int P) {
 static int nh_for(int M) { return M <= 128 ? 64 : 96; }
 static int ak_for(int nh) { return nh <= 64 ? 256 : 128; }
 
-static bool few(const sv_w4 *w, int M) { return M <= kFewTokens && few_smem(M, w->H) <= kFewSmem; }
+static bool few(const sv_w4 *w, int M) {
+    return M <= kFewTokens && w->V >= kFewRows && few_smem(M, w->H) <= kFewSmem;
+}
 
 struct HeadPlan {
     size_t off_rows, off_image, bytes;
