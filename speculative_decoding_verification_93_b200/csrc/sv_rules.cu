@@ -4,19 +4,21 @@
 //
 // The rules change few logits: the tokens a request has seen (a few thousand
 // of 129280), its biased tokens, and what its grammar forbids.  So nothing
-// walks the vocabulary logit by logit.  One CTA takes kChunk tokens of one
-// row and every scheduled position of that chunk:
+// walks the vocabulary rule by rule.  One CTA takes a chunk of one row's
+// vocabulary and every scheduled position of that chunk:
 //   A. the chunk's bit planes (prompt, output; drafts and biases are OR-ed
 //      in) are read once, V / 8 bytes each, and compacted into a list of the
 //      touched tokens in shared memory;
-//   B. per position, 16-byte units: in place, units whose mask byte forbids
-//      all eight (fp32: four) logits are overwritten without being read, and
-//      mixed units are written element by element; with a separate output
-//      the unit is copied with the forbidden elements replaced;
-//   C. (position, list entry) pairs over all threads: read the logit and its
-//      count, apply the penalties, write;  D. the same for biased tokens.
-// In place, B and C/D touch disjoint elements (forbidden, allowed); with a
-// separate output a barrier orders them.
+//   B. in place, 16-byte units of the masked positions: units a mask forbids
+//      whole are overwritten without being read, mixed ones written element by
+//      element; with a separate output every unit is copied, masked on the way;
+//   C. the touched tokens, one (token, position) a thread: logit, mask word
+//      and count are requested together, the penalised logit is written.  With
+//      a separate output this follows each position's copy, while its lines
+//      are still in the caches.  (Penalising inside the copy was slower, 66
+//      against 59 us at 64 x 5 x 129280 bf16: a few lanes of a warp had work.)
+//   D. the chunk's biased tokens, one (entry, position) a thread.
+// In place, B and C/D touch disjoint elements (forbidden, allowed).
 #include <climits>
 #include <cstdint>
 
@@ -26,8 +28,17 @@
 
 namespace sv {
 
-constexpr int kRuleThreads = 256;
-constexpr int kChunk = 32 * kRuleThreads;   // tokens per CTA: one bit-plane word per thread
+constexpr int kBiasList = 256;
+
+// In place a CTA mostly waits (for its row's parameters, its planes, then a few
+// logits each), so it takes many tokens; a copy is bound by its bytes, and small
+// CTAs keep more of them on their way.
+template <bool IN_PLACE> struct RuleCfg {
+    static constexpr int kThreads = IN_PLACE ? 256 : 128;
+    static constexpr int kPlane = IN_PLACE ? kThreads : kThreads / 2;   // words of a plane
+    static constexpr int kChunk = 32 * kPlane;           // tokens
+    static constexpr int kResident = IN_PLACE ? 5 : 8;   // CTAs on an SM
+};
 
 struct RuleArgs {
     const char *in;
@@ -65,18 +76,34 @@ template <int ESIZE> __device__ __forceinline__ float ld_logit(const char *p) {
     return __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const unsigned short *>(p)) << 16);
 }
 
+// The bits of a logit, to be widened once every load of a batch is out: a
+// conversion right behind its load would wait for it.
+template <int ESIZE> __device__ __forceinline__ uint32_t ld_raw(const char *p) {
+    if (ESIZE == 4) return *reinterpret_cast<const uint32_t *>(p);
+    return *reinterpret_cast<const unsigned short *>(p);
+}
+template <int ESIZE> __device__ __forceinline__ float widen(uint32_t raw) {
+    return __uint_as_float(ESIZE == 4 ? raw : raw << 16);
+}
+
 template <int ESIZE> __device__ __forceinline__ void st_logit(char *p, float z) {
     if (ESIZE == 4) *reinterpret_cast<float *>(p) = z;
     else *reinterpret_cast<__nv_bfloat16 *>(p) = __float2bfloat16_rn(z);
 }
 
-struct RuleSmem {
-    uint32_t draft[kRuleThreads];    // planes of the chunk, bit = local token
-    uint32_t bias[kRuleThreads];
-    uint32_t prompt[kRuleThreads];
-    uint32_t output[kRuleThreads];
-    unsigned short list[kChunk];     // touched local tokens without a bias
-    int n;
+template <bool IN_PLACE> struct RuleSmem {
+    using Cfg = RuleCfg<IN_PLACE>;
+    uint32_t draft[Cfg::kPlane];     // planes of the chunk, bit = local token
+    uint32_t bias[Cfg::kPlane];
+    uint32_t prompt[Cfg::kPlane];
+    uint32_t output[Cfg::kPlane];
+    unsigned short list[Cfg::kChunk];   // touched tokens without a bias, ascending
+    int count[IN_PLACE ? 1 : Cfg::kChunk];   // output count of each listed token
+    int wsum[Cfg::kThreads / 32];
+    int nbias;                       // valid biases of this chunk, and the first of them:
+    int blist[kBiasList];            //   entry
+    unsigned short btoken[kBiasList];   //   local token
+    float bvalue[kBiasList];
     int dup;                         // a biased token of this chunk is listed twice
     int dtok[SV_MAX_K];              // local token of each draft, -1 if not in the chunk
     int mask[SV_MAX_K + 1];          // mask of each position, -1 for none
@@ -112,34 +139,24 @@ __device__ __forceinline__ bool allowed(const uint32_t *mask, int v) {
     return !mask || (__ldg(mask + (v >> 5)) >> (v & 31) & 1u);
 }
 
-// What a token's history says: its count before the block, the prompt's bit,
-// and whether the block's drafts name it.
-struct TokenState {
-    int count;
-    bool prompt, draft;
-};
-
-__device__ __forceinline__ TokenState token_state(const RuleArgs &a, const RowRules &r, const RuleSmem &sm,
-                                                  int c0, int lv) {
-    const uint32_t bit = 1u << (lv & 31);
-    TokenState s;
-    s.count = 0;
-    if (sm.output[lv >> 5] & bit)
-        s.count = __ldg(a.counts + static_cast<long long>(r.slot) * a.V + a.v0 + c0 + lv);
-    s.prompt = sm.prompt[lv >> 5] & bit;
-    s.draft = sm.draft[lv >> 5] & bit;
-    return s;
+// Output count of token lv of the chunk at c0.
+template <bool IN_PLACE>
+__device__ __forceinline__ int output_count(const RuleArgs &a, const RowRules &r, const RuleSmem<IN_PLACE> &sm,
+                                            int c0, int lv) {
+    return sm.output[lv >> 5] >> (lv & 31) & 1u
+               ? __ldg(a.counts + static_cast<long long>(r.slot) * a.V + a.v0 + c0 + lv) : 0;
 }
 
-// Penalties of a token at position p, on logit z.
-__device__ __forceinline__ float penalise(const RuleArgs &a, const RowRules &r, const RuleSmem &sm,
-                                          const TokenState &s, int lv, int p, int ndraft, float z) {
-    int c = s.count;
-    if (s.draft) {
+// Penalties of token lv at position p, on logit z; c: its output count.
+template <bool IN_PLACE>
+__device__ __forceinline__ float penalise(const RuleArgs &a, const RowRules &r, const RuleSmem<IN_PLACE> &sm,
+                                          int lv, int c, int p, int ndraft, float z) {
+    const uint32_t bit = 1u << (lv & 31);
+    if (sm.draft[lv >> 5] & bit) {
         const int before = min(a.pos0 + p, ndraft);
         for (int j = 0; j < before; ++j) c += sm.dtok[j] == lv;
     }
-    if (c > 0 || s.prompt) z = z > 0.f ? z / r.rep : z * r.rep;
+    if (c > 0 || (sm.prompt[lv >> 5] & bit)) z = z > 0.f ? z / r.rep : z * r.rep;
     z -= r.freq * static_cast<float>(c);
     if (c > 0) z -= r.pres;
     return z;
@@ -168,73 +185,158 @@ template <int N> __device__ __forceinline__ uint32_t mask_bits(const uint32_t *m
     return bits & ((1u << N) - 1u);
 }
 
-// B. Position p of the chunk: masks, and the copy when the output is separate.
-template <int ESIZE, bool IN_PLACE, bool MASKED>
-__device__ __forceinline__ void mask_position(const RuleArgs &a, int b, int p, int c0, int n, const uint32_t *mask) {
+// The 16-byte units u0 .. u1 - 1 of a vector's elements c0 .. c0 + n - 1 (unit u
+// starts at element head + kPer u), and the single elements beside them:
+// [c0, first) and [last, c0 + n).
+struct Units {
+    int head, u0, u1, first, last;
+};
+
+template <int ESIZE> __device__ __forceinline__ Units units_of(const char *vec, int c0, int n, bool any) {
+    constexpr int kPer = 16 / ESIZE;
+    Units s;
+    const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(vec) & 15u);
+    s.head = mis ? (16 - mis) / ESIZE : 0;
+    s.u0 = s.u1 = 0;
+    s.first = s.last = c0 + n;
+    if (any) {
+        s.u0 = c0 <= s.head ? 0 : (c0 - s.head + kPer - 1) / kPer;
+        s.u1 = c0 + n <= s.head ? 0 : (c0 + n - s.head) / kPer;
+        if (s.u1 > s.u0) { s.first = s.head + kPer * s.u0; s.last = s.head + kPer * s.u1; }
+    }
+    return s;
+}
+
+// B in place: -inf wherever a mask forbids.  A warp takes 128 units: each lane
+// reads one word of the mask (of four positions at a time, so that a chunk's
+// masks cost one or two round trips) and hands its units' bits round.
+template <int ESIZE>
+__device__ __forceinline__ void forbid(const RuleArgs &a, const RuleSmem<true> &sm, int b, int np, int c0, int n) {
+    constexpr int kPer = 16 / ESIZE, kAhead = 4, kSpan = 128, kWords = kSpan * kPer / 32, kUnits = 32 / kPer;
+    constexpr uint32_t kAll = (1u << kPer) - 1u;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const char *row = a.out + static_cast<long long>(b) * a.P * a.Vs * ESIZE;
+    const long long vec = static_cast<long long>(a.Vs) * ESIZE;
+    constexpr int kSpans = RuleCfg<true>::kChunk / kPer / kSpan + 1;
+    for (int span = warp; span < kSpans; span += RuleCfg<true>::kThreads / 32) {
+        for (int p0 = 0; p0 < np; p0 += kAhead) {
+            uint32_t w[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                w[k] = ~0u;
+                const int m = p0 + k < np ? sm.mask[p0 + k] : -1;
+                if (m >= 0 && lane < kWords) {
+                    const Units s = units_of<ESIZE>(row + (p0 + k) * vec, c0, n, true);
+                    const int v = a.v0 + s.head + kPer * (s.u0 + span * kSpan) + 32 * lane;
+                    w[k] = bits32(a.mask + static_cast<long long>(m) * a.W, a.W, v);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (p0 + k >= np || sm.mask[p0 + k] < 0) continue;
+                const Units s = units_of<ESIZE>(row + (p0 + k) * vec, c0, n, true);
+#pragma unroll
+                for (int i = 0; i < kSpan / 32; ++i) {
+                    const int u = s.u0 + span * kSpan + 32 * i + lane;
+                    const uint32_t keep =
+                        __shfl_sync(0xffffffffu, w[k], (32 * i + lane) / kUnits) >> (lane % kUnits * kPer) & kAll;
+                    char *d = const_cast<char *>(row) + (p0 + k) * vec + static_cast<long long>(s.head + kPer * u) * ESIZE;
+                    if (u >= s.u1) continue;
+                    if (keep == 0) {
+                        *reinterpret_cast<uint4 *>(d) = mask_unit<ESIZE>(make_uint4(0, 0, 0, 0), 0);
+                    } else {
+                        for (uint32_t f = keep ^ kAll; f; f &= f - 1) st_logit<ESIZE>(d + (__ffs(f) - 1) * ESIZE, kNegInf);
+                    }
+                }
+            }
+        }
+    }
+    // The elements before the first unit and behind the last.
+    for (int q = tid; q < np * 2 * kPer; q += RuleCfg<true>::kThreads) {
+        const int p = q / (2 * kPer), i = q % (2 * kPer);
+        if (sm.mask[p] < 0) continue;
+        const Units s = units_of<ESIZE>(row + p * vec, c0, n, true);
+        const int before = s.first - c0, v = i < before ? c0 + i : s.last + i - before;
+        if (v < c0 + n && !allowed(mask_row(a, sm.mask[p]), a.v0 + v))
+            st_logit<ESIZE>(const_cast<char *>(row) + p * vec + static_cast<long long>(v) * ESIZE, kNegInf);
+    }
+}
+
+// B with a separate output: position p of the chunk, copied and masked.
+template <int ESIZE, bool MASKED>
+__device__ __forceinline__ void copy_position(const RuleArgs &a, int b, int p, int c0, int n, const uint32_t *mask) {
     constexpr int kPer = 16 / ESIZE, kBatch = 4;
     constexpr uint32_t kAll = (1u << kPer) - 1u;
     const int tid = threadIdx.x;
     const long long vec = (static_cast<long long>(b) * a.P + p) * a.Vs;
     const char *src = a.in + vec * ESIZE;
     char *dst = a.out + vec * ESIZE;
-    // Units start at the elements head + kPer u of the vector.
-    const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(dst) & 15u);
-    const int head = mis ? (16 - mis) / ESIZE : 0;
-    int u0 = 0, u1 = 0, first = c0 + n, last = c0 + n;   // single elements: [c0, first) and [last, c0 + n)
-    if (IN_PLACE || ((reinterpret_cast<uintptr_t>(src) ^ reinterpret_cast<uintptr_t>(dst)) & 15u) == 0) {
-        u0 = c0 <= head ? 0 : (c0 - head + kPer - 1) / kPer;
-        u1 = c0 + n <= head ? 0 : (c0 + n - head) / kPer;
-        if (u1 > u0) { first = head + kPer * u0; last = head + kPer * u1; }
-    }
+    const Units s = units_of<ESIZE>(dst, c0, n, ((reinterpret_cast<uintptr_t>(src) ^ reinterpret_cast<uintptr_t>(dst)) & 15u) == 0);
     // kBatch units a thread: all their loads before the first store.
-    for (int base = u0 + tid; base < u1; base += kBatch * kRuleThreads) {
+    for (int base = s.u0 + tid; base < s.u1; base += kBatch * RuleCfg<false>::kThreads) {
         uint32_t keep[kBatch];
         uint4 data[kBatch];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int u = base + k * kRuleThreads;
+            const int u = base + k * RuleCfg<false>::kThreads;
             keep[k] = kAll;
-            if (u < u1) {
-                if (!IN_PLACE) data[k] = ld_stream(src + static_cast<long long>(head + kPer * u) * ESIZE);
-                if (MASKED) keep[k] = mask_bits<kPer>(mask, a.W, a.v0 + head + kPer * u);
+            if (u < s.u1) {
+                data[k] = ld_stream(src + static_cast<long long>(s.head + kPer * u) * ESIZE);
+                if (MASKED) keep[k] = mask_bits<kPer>(mask, a.W, a.v0 + s.head + kPer * u);
             }
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int u = base + k * kRuleThreads;
-            char *d = dst + static_cast<long long>(head + kPer * u) * ESIZE;
-            if (u >= u1) continue;
-            if (!IN_PLACE) {
-                *reinterpret_cast<uint4 *>(d) = MASKED ? mask_unit<ESIZE>(data[k], keep[k]) : data[k];
-            } else if (keep[k] == 0) {
-                *reinterpret_cast<uint4 *>(d) = mask_unit<ESIZE>(make_uint4(0, 0, 0, 0), 0);
-            } else {
-                for (uint32_t m = keep[k] ^ kAll; m; m &= m - 1) st_logit<ESIZE>(d + (__ffs(m) - 1) * ESIZE, kNegInf);
-            }
+            const int u = base + k * RuleCfg<false>::kThreads;
+            if (u < s.u1)
+                *reinterpret_cast<uint4 *>(dst + static_cast<long long>(s.head + kPer * u) * ESIZE) =
+                    MASKED ? mask_unit<ESIZE>(data[k], keep[k]) : data[k];
         }
     }
-    const int nscalar = (first - c0) + (c0 + n - last);
-    for (int q = tid; q < nscalar; q += kRuleThreads) {
-        const int v = q < first - c0 ? c0 + q : last + (q - (first - c0));
-        if (MASKED && !allowed(mask, a.v0 + v))
+    const int nscalar = (s.first - c0) + (c0 + n - s.last);
+    for (int q = tid; q < nscalar; q += RuleCfg<false>::kThreads) {
+        const int v = q < s.first - c0 ? c0 + q : s.last + (q - (s.first - c0));
+        if (MASKED && !allowed(mask, a.v0 + v)) {
             st_logit<ESIZE>(dst + static_cast<long long>(v) * ESIZE, kNegInf);
-        else if (!IN_PLACE)
-            st_logit<ESIZE>(dst + static_cast<long long>(v) * ESIZE, ld_logit<ESIZE>(src + static_cast<long long>(v) * ESIZE));
+        } else {                         // bits, not numbers: NaN payloads stay
+            if (ESIZE == 4) reinterpret_cast<uint32_t *>(dst)[v] = reinterpret_cast<const uint32_t *>(src)[v];
+            else reinterpret_cast<unsigned short *>(dst)[v] = reinterpret_cast<const unsigned short *>(src)[v];
+        }
     }
 }
 
 __device__ __forceinline__ bool valid_bias(float v) { return !isnan(v) && !(isinf(v) && v > 0.f); }
 
+// Status: the row's parameters, and masks of its first np positions that allow
+// nothing (a row's CTAs share them).
+template <bool IN_PLACE>
+__device__ __forceinline__ void report(const RuleArgs &a, const RuleSmem<IN_PLACE> &sm, int chunk, int np, int bits) {
+    if (!a.status) return;
+    for (int p = chunk; p < np; p += a.nchunk) {
+        const uint32_t *mask = mask_row(a, sm.mask[p]);
+        if (!mask) continue;
+        uint32_t any = 0;
+        for (int w = threadIdx.x; w < a.W && !any; w += RuleCfg<IN_PLACE>::kThreads) {
+            any = __ldg(mask + w);
+            if (w == a.W - 1 && (a.V & 31)) any &= (1u << (a.V & 31)) - 1u;
+        }
+        if (!__syncthreads_or(any != 0) && threadIdx.x == 0) bits |= SV_ROW_EMPTY_MASK;
+    }
+    if (bits) atomicOr(a.status, bits);
+}
+
 template <int ESIZE, bool IN_PLACE>
-__global__ void __launch_bounds__(kRuleThreads) rules_kernel(RuleArgs a) {
-    __shared__ RuleSmem sm;
-    constexpr int kBatch = 4;
-    const int tid = threadIdx.x;
+__global__ void __launch_bounds__(RuleCfg<IN_PLACE>::kThreads, RuleCfg<IN_PLACE>::kResident) rules_kernel(RuleArgs a) {
+    using Cfg = RuleCfg<IN_PLACE>;
+    __shared__ RuleSmem<IN_PLACE> sm;
+    constexpr int kThreads = Cfg::kThreads;
+    constexpr int kTokens = 2;           // touched tokens on their way at a time
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // Rows fastest: the low chunks, where most of a text's tokens lie, first.
     const int chunk = blockIdx.x / a.B, b = blockIdx.x - chunk * a.B;
+    const int c0 = chunk * Cfg::kChunk, n = min(Cfg::kChunk, a.Vs - c0);
     griddep_wait();
     griddep_launch_dependents();
-    const int c0 = chunk * kChunk, n = min(kChunk, a.Vs - c0);
 
     // Everything about the row in one round trip.
     const int len = a.lengths ? __ldg(a.lengths + b) : 0;
@@ -262,8 +364,13 @@ __global__ void __launch_bounds__(kRuleThreads) rules_kernel(RuleArgs a) {
         if (tid < np) bits |= SV_ROW_BAD_MASK;
     }
     const bool penal = r.rep != 1.f || r.freq != 0.f || r.pres != 0.f;
-
-    // A. Planes of the chunk, drafts and biases.
+    const int ndraft = min(a.K, a.pos0 + np - 1);   // drafts before the last position
+    if (tid < ndraft && (x < 0 || x >= a.V)) bits |= SV_ROW_BAD_TOKEN;
+    if (tid <= SV_MAX_K) sm.mask[tid] = m;
+    if (tid == 0) sm.dup = sm.nbias = 0;
+    for (int w = tid; w < Cfg::kPlane; w += kThreads) sm.draft[w] = sm.bias[w] = 0;
+    // The planes, and the bias list's first entries, are on their way over the
+    // barrier.
     uint32_t wp = 0, wo = 0;
     if (penal && r.slot >= 0 && 32 * tid < n) {
         const uint32_t live = n - 32 * tid >= 32 ? ~0u : (1u << (n - 32 * tid)) - 1u;
@@ -271,104 +378,174 @@ __global__ void __launch_bounds__(kRuleThreads) rules_kernel(RuleArgs a) {
         wo = bits32(a.output + row, a.W, a.v0 + c0 + 32 * tid) & live;
         if (r.rep != 1.f) wp = bits32(a.prompt + row, a.W, a.v0 + c0 + 32 * tid) & live;
     }
-    const int ndraft = min(a.K, a.pos0 + np - 1);   // drafts before the last position
-    if (tid == 0) { sm.n = 0; sm.dup = 0; }
-    if (tid <= SV_MAX_K) sm.mask[tid] = m;
-    sm.draft[tid] = 0;
-    sm.bias[tid] = 0;
-    sm.prompt[tid] = wp;
-    sm.output[tid] = wo;
-    __syncthreads();
+    int bt = -1;
+    float bv = 0.f;
+    if (e0 + tid < e1) {
+        bt = __ldg(a.bias_tokens + e0 + tid);
+        bv = __ldg(a.bias_values + e0 + tid);
+    }
+    const bool masked = __syncthreads_or(tid < np && m >= 0);
+    if constexpr (IN_PLACE) {
+        if (masked) forbid<ESIZE>(a, sm, b, np, c0, n);
+        if (!penal && e0 == e1) {                         // no more rules
+            report(a, sm, chunk, masked ? np : 0, bits);
+            return;
+        }
+    }
+    // A. Planes of the chunk, drafts and biases.
     if (tid < ndraft) {
         int lv = -1;
-        if (x < 0 || x >= a.V) bits |= SV_ROW_BAD_TOKEN;
-        else if (x >= a.v0 + c0 && x < a.v0 + c0 + n) lv = x - a.v0 - c0;
+        if (x >= 0 && x < a.V && x >= a.v0 + c0 && x < a.v0 + c0 + n) lv = x - a.v0 - c0;
         sm.dtok[tid] = lv;
         if (lv >= 0 && penal) atomicOr(&sm.draft[lv >> 5], 1u << (lv & 31));
     }
-    for (int e = e0 + tid; e < e1; e += kRuleThreads) {
-        const int t = __ldg(a.bias_tokens + e);
-        const float v = __ldg(a.bias_values + e);
-        if (t < 0 || t >= a.V) { bits |= SV_ROW_BAD_TOKEN; continue; }
-        if (!valid_bias(v)) { bits |= SV_ROW_BAD_BIAS; continue; }
-        const int lv = t - a.v0 - c0;
+    for (int e = e0 + tid; e < e1; e += kThreads) {
+        if (e != e0 + tid) {
+            bt = __ldg(a.bias_tokens + e);
+            bv = __ldg(a.bias_values + e);
+        }
+        if (bt < 0 || bt >= a.V) { bits |= SV_ROW_BAD_TOKEN; continue; }
+        if (!valid_bias(bv)) { bits |= SV_ROW_BAD_BIAS; continue; }
+        const int lv = bt - a.v0 - c0;
         if (lv < 0 || lv >= n) continue;
         const uint32_t bit = 1u << (lv & 31);
         if (atomicOr(&sm.bias[lv >> 5], bit) & bit) sm.dup = 1;
+        const int i = atomicAdd(&sm.nbias, 1);
+        if (i < kBiasList) {
+            sm.blist[i] = e;
+            sm.btoken[i] = static_cast<unsigned short>(lv);
+            sm.bvalue[i] = bv;
+        }
+    }
+    if (tid < Cfg::kPlane) {
+        sm.prompt[tid] = wp;
+        sm.output[tid] = wo;
     }
     __syncthreads();
-    uint32_t touched = (wp | wo | sm.draft[tid]) & ~sm.bias[tid];
-    if (touched) {
-        int at = atomicAdd(&sm.n, __popc(touched));
-        for (; touched; touched &= touched - 1) sm.list[at++] = 32 * tid + __ffs(touched) - 1;
+    // The touched tokens in ascending order: places by a scan over the words.
+    uint32_t touched = tid < Cfg::kPlane ? (wp | wo | sm.draft[tid]) & ~sm.bias[tid] : 0u;
+    int incl = __popc(touched);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
     }
-
-    // B. Masks, and the copy when the output is separate.
-    for (int p = 0; p < np; ++p) {
-        const uint32_t *mask = mask_row(a, sm.mask[p]);
-        if (mask) mask_position<ESIZE, IN_PLACE, true>(a, b, p, c0, n, mask);
-        else if (!IN_PLACE) mask_position<ESIZE, IN_PLACE, false>(a, b, p, c0, n, nullptr);
+    if (lane == 31) sm.wsum[warp] = incl;
+    __syncthreads();
+    int at = incl - __popc(touched), ntouched = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) at += sm.wsum[w];
+        ntouched += sm.wsum[w];
     }
+    for (; touched; touched &= touched - 1) sm.list[at++] = 32 * tid + __ffs(touched) - 1;
     __syncthreads();
 
-    // C. Penalised tokens without a bias: a token a thread, kBatch positions
-    // on their way at a time.
-    const long long row_at = (static_cast<long long>(b) * a.P * a.Vs + c0) * ESIZE;
     const long long vec = static_cast<long long>(a.Vs) * ESIZE;
-    for (int q = tid; q < sm.n; q += kRuleThreads) {
-        const int lv = sm.list[q];
-        const TokenState s = token_state(a, r, sm, c0, lv);
-        for (int p0 = 0; p0 < np; p0 += kBatch) {
-            float z[kBatch];
-            bool live[kBatch];
+    const long long row_at = (static_cast<long long>(b) * a.P * a.Vs + c0) * ESIZE;
+    if (!IN_PLACE) {
+        for (int q = tid; q < ntouched; q += kThreads) sm.count[q] = output_count(a, r, sm, c0, sm.list[q]);
+        for (int p = 0; p < np; ++p) {
+            const uint32_t *mask = mask_row(a, sm.mask[p]);
+            const char *src = a.in + row_at + p * vec;
+            char *dst = a.out + row_at + p * vec;
+            // C's first logits are on their way during the copy.
+            uint32_t z[kTokens], word[kTokens];
+            auto ask = [&](int q0) {
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int p = p0 + k;
-                live[k] = p < np && allowed(mask_row(a, sm.mask[p]), a.v0 + c0 + lv);
-                if (live[k]) z[k] = ld_logit<ESIZE>(a.in + row_at + p * vec + lv * ESIZE);
+                for (int k = 0; k < kTokens; ++k) {
+                    const int q = q0 + k * kThreads, lv = q < ntouched ? sm.list[q] : 0;
+                    z[k] = ld_raw<ESIZE>(src + lv * ESIZE);
+                    word[k] = ~0u;
+                    if (mask) word[k] = __ldg(mask + ((a.v0 + c0 + lv) >> 5));
+                }
+            };
+            if (ntouched) ask(tid);
+            if (mask) copy_position<ESIZE, true>(a, b, p, c0, n, mask);
+            else copy_position<ESIZE, false>(a, b, p, c0, n, nullptr);
+            __syncthreads();
+            for (int q0 = tid; q0 < ntouched; q0 += kTokens * kThreads) {
+                if (q0 != tid) ask(q0);
+#pragma unroll
+                for (int k = 0; k < kTokens; ++k) {
+                    const int q = q0 + k * kThreads;
+                    if (q >= ntouched) break;
+                    const int lv = sm.list[q];
+                    if (word[k] >> ((a.v0 + c0 + lv) & 31) & 1u)
+                        st_logit<ESIZE>(dst + lv * ESIZE,
+                                        penalise(a, r, sm, lv, sm.count[q], p, ndraft, widen<ESIZE>(z[k])));
+                }
             }
+        }
+        __syncthreads();
+    } else {
+        // C. Tokens fastest.  A forbidden logit is read too: waiting for its
+        // mask first would cost a second round trip.
+        if (ntouched > 0) {
+            const int dq = kThreads / ntouched, dr = kThreads % ntouched;
+            int q = tid % ntouched, p = tid / ntouched;
+            while (p < np) {
+                uint32_t z[kTokens], word[kTokens];
+                int lv[kTokens], at_p[kTokens], c[kTokens];
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                if (live[k])
-                    st_logit<ESIZE>(a.out + row_at + (p0 + k) * vec + lv * ESIZE,
-                                    penalise(a, r, sm, s, lv, p0 + k, ndraft, z[k]));
+                for (int k = 0; k < kTokens; ++k) {
+                    at_p[k] = p;
+                    lv[k] = sm.list[q];
+                    word[k] = ~0u;
+                    if (p < np) {
+                        z[k] = ld_raw<ESIZE>(a.in + row_at + p * vec + lv[k] * ESIZE);
+                        c[k] = output_count(a, r, sm, c0, lv[k]);
+                        if (masked)
+                            if (const uint32_t *mask = mask_row(a, sm.mask[p])) word[k] = __ldg(mask + ((a.v0 + c0 + lv[k]) >> 5));
+                    }
+                    q += dr;
+                    p += dq;
+                    if (q >= ntouched) { q -= ntouched; ++p; }
+                }
+#pragma unroll
+                for (int k = 0; k < kTokens; ++k)
+                    if (at_p[k] < np && (word[k] >> ((a.v0 + c0 + lv[k]) & 31) & 1u))
+                        st_logit<ESIZE>(a.out + row_at + at_p[k] * vec + lv[k] * ESIZE,
+                                        penalise(a, r, sm, lv[k], c[k], at_p[k], ndraft, widen<ESIZE>(z[k])));
+            }
         }
     }
     // D. Biased tokens: the last entry of a token counts.
-    const long long pairs = static_cast<long long>(e1 - e0) * np;
-    for (long long q = tid; q < pairs; q += kRuleThreads) {
-        const int e = e0 + static_cast<int>(q / np), p = static_cast<int>(q % np);
-        const int t = __ldg(a.bias_tokens + e), lv = t - a.v0 - c0;
-        if (t < 0 || t >= a.V || lv < 0 || lv >= n) continue;
-        const float v = __ldg(a.bias_values + e);
-        if (!valid_bias(v)) continue;
-        if (sm.dup) {
-            bool later = false;
-            for (int f = e + 1; f < e1 && !later; ++f)
-                later = __ldg(a.bias_tokens + f) == t && valid_bias(__ldg(a.bias_values + f));
-            if (later) continue;
+    if (sm.nbias > 0) {
+        const bool listed = sm.nbias <= kBiasList;
+        const long long pairs = static_cast<long long>(listed ? sm.nbias : e1 - e0) * np;
+        for (long long q = tid; q < pairs; q += kThreads) {
+            const int i = static_cast<int>(q / np), p = static_cast<int>(q - static_cast<long long>(i) * np);
+            int e = e0 + i, lv;
+            float v;
+            if (listed) {
+                e = sm.blist[i];
+                lv = sm.btoken[i];
+                v = sm.bvalue[i];
+            } else {
+                const int t = __ldg(a.bias_tokens + e);
+                lv = t - a.v0 - c0;
+                v = __ldg(a.bias_values + e);
+                if (t < 0 || t >= a.V || lv < 0 || lv >= n || !valid_bias(v)) continue;
+            }
+            const int t = a.v0 + c0 + lv;
+            if (sm.dup) {
+                bool later = false;
+                for (int f = e + 1; f < e1 && !later; ++f)
+                    later = __ldg(a.bias_tokens + f) == t && valid_bias(__ldg(a.bias_values + f));
+                if (later) continue;
+            }
+            const long long to = row_at + p * vec + lv * ESIZE;
+            const uint32_t raw = ld_raw<ESIZE>(a.in + to);
+            const int c = penal ? output_count(a, r, sm, c0, lv) : 0;
+            if (!allowed(mask_row(a, sm.mask[p]), t)) continue;
+            float z = widen<ESIZE>(raw);
+            if (penal) z = penalise(a, r, sm, lv, c, p, ndraft, z);
+            st_logit<ESIZE>(a.out + to, z + v);
         }
-        if (!allowed(mask_row(a, sm.mask[p]), t)) continue;
-        const long long at = row_at + p * vec + lv * ESIZE;
-        float z = ld_logit<ESIZE>(a.in + at);
-        if (penal) z = penalise(a, r, sm, token_state(a, r, sm, c0, lv), lv, p, ndraft, z);
-        st_logit<ESIZE>(a.out + at, z + v);
     }
 
-    // Status: the row's parameters, and masks that allow nothing (a row's
-    // CTAs share its positions).
-    if (!a.status) return;
-    for (int p = chunk; p < np; p += a.nchunk) {
-        const uint32_t *mask = mask_row(a, sm.mask[p]);
-        if (!mask) continue;
-        uint32_t any = 0;
-        for (int w = tid; w < a.W && !any; w += kRuleThreads) {
-            any = __ldg(mask + w);
-            if (w == a.W - 1 && (a.V & 31)) any &= (1u << (a.V & 31)) - 1u;
-        }
-        if (!__syncthreads_or(any != 0) && tid == 0) bits |= SV_ROW_EMPTY_MASK;
-    }
-    if (bits) atomicOr(a.status, bits);
+    report(a, sm, chunk, masked ? np : 0, bits);
 }
 
 }  // namespace sv
@@ -410,7 +587,9 @@ extern "C" sv_status sv_logits_process(const void *logits, void *out, sv_dtype d
     a.out = static_cast<char *>(out);
     a.B = B; a.P = P; a.V = V; a.v0 = v0; a.Vs = Vs;
     a.W = (V + 31) / 32;
-    a.nchunk = (Vs + sv::kChunk - 1) / sv::kChunk;
+    const bool in_place = in_at == out_at;
+    const int chunk = in_place ? sv::RuleCfg<true>::kChunk : sv::RuleCfg<false>::kChunk;
+    a.nchunk = (Vs + chunk - 1) / chunk;
     a.drafts = K > 0 ? draft_tokens : nullptr;
     a.K = K; a.pos0 = pos0;
     a.lengths = lengths; a.extra = extra;
@@ -423,10 +602,9 @@ extern "C" sv_status sv_logits_process(const void *logits, void *out, sv_dtype d
     a.status = status;
     const long long grid = static_cast<long long>(B) * a.nchunk;
     if (grid > INT_MAX) return SV_ERR_SHAPE;
-    const bool in_place = in_at == out_at;
     auto *kernel = dtype == SV_F32 ? (in_place ? sv::rules_kernel<4, true> : sv::rules_kernel<4, false>)
                                    : (in_place ? sv::rules_kernel<2, true> : sv::rules_kernel<2, false>);
     return sv::note_cuda(sv::launch_pdl(kernel, dim3(static_cast<unsigned>(grid)),
-                                        dim3(sv::kRuleThreads), 0,
+                                        dim3(in_place ? sv::RuleCfg<true>::kThreads : sv::RuleCfg<false>::kThreads), 0,
                                         static_cast<cudaStream_t>(stream), a));
 }
