@@ -406,29 +406,42 @@ class _W4(ctypes.Structure):
                 ("group", ctypes.c_int)]
 
 
-def _given(t, dtype, name: str, like: torch.Tensor, shape=None):
-    """An optional tensor argument on the device of `like`: its address, or None."""
+# The raw handle of the current stream, without a Stream object around it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _given(t, dtype, name: str, dev: int, shape=None):
+    """An optional tensor argument on device `dev` (-1: the host): its address, or
+    None."""
     if t is None:
         return None
     if t.dtype != dtype or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous {dtype} tensor")
-    if t.device != like.device:
-        raise TypeError(f"{name} must be on {like.device}, is on {t.device}")
-    if shape is not None and tuple(t.shape) != shape:
+    if t.get_device() != dev:
+        raise TypeError(f"{name} must be on {f'cuda:{dev}' if dev >= 0 else 'cpu'}, "
+                        f"is on {t.device}")
+    if shape is not None and t.shape != shape:
         raise TypeError(f"{name} must have the shape {shape}, has {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _call(fn: str, like: torch.Tensor, stream, *args) -> None:
-    """Call `fn` on the device of `like`, with the stream as the last argument."""
-    if not like.is_cuda:
+def _call(fn: str, dev: int, stream, *args) -> None:
+    """Call `fn` on device `dev`, with the stream (default: the current one of
+    that device) as the last argument."""
+    if dev < 0:
         raise TypeError(f"{fn}: the tensors must be on a GPU")
-    st = _stream(stream, like)
-    if like.device.index == torch.cuda.current_device():
-        _check(fn, getattr(lib(), fn)(*args, st))
+    if stream is None:
+        stream = _raw_stream(dev)
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        code = getattr(lib(), fn)(*args, int(stream))
     else:
-        with torch.cuda.device(like.device):
-            _check(fn, getattr(lib(), fn)(*args, st))
+        with torch.cuda.device(dev):
+            code = getattr(lib(), fn)(*args, int(stream))
+    if code != 0:
+        raise SVError(fn, code)
 
 
 class TokenHistory:
@@ -437,12 +450,13 @@ class TokenHistory:
 
     def __init__(self, V: int, prompt_bits, output_bits, output_counts):
         R, W = output_counts.shape[0], (V + 31) // 32
-        at = [_given(t, torch.int32, name, output_counts, shape) for name, t, shape in (
+        dev = output_counts.get_device()
+        at = [_given(t, torch.int32, name, dev, shape) for name, t, shape in (
             ("prompt_bits", prompt_bits, (R, W)), ("output_bits", output_bits, (R, W)),
             ("output_counts", output_counts, (R, V)))]
         self.prompt_bits, self.output_bits = prompt_bits, output_bits
         self.output_counts = output_counts
-        self.R, self.V = R, V
+        self.R, self.V, self.dev = R, V, dev
         self.desc = _History(*at, R, V)
 
     @classmethod
@@ -466,17 +480,17 @@ class LogitRules:
                 ("frequency", frequency, f32), ("presence", presence, f32))
         given = [t for _, t, _ in rows] + [bias_begin, mask, mask_index]
         given += [] if history is None else [history.output_counts]
-        like = next((t for t in given if t is not None), None)
+        dev = next((t.get_device() for t in given if t is not None), None)
         n = None
         at = []
         for name, t, dtype in rows:
-            at.append(_given(t, dtype, name, like))
+            at.append(_given(t, dtype, name, dev))
             if t is not None:
                 if t.dim() != 1 or n not in (None, t.numel()):
                     raise TypeError("the per-row tensors must be vectors of the same length")
                 n = t.numel()
         if history is not None:
-            _given(history.output_counts, i32, "history", like)
+            _given(history.output_counts, i32, "history", dev)
         if (bias_begin is None) != (bias_tokens is None) or \
                 (bias_begin is None) != (bias_values is None):
             raise TypeError("bias_begin, bias_tokens and bias_values go together")
@@ -486,9 +500,9 @@ class LogitRules:
             if n not in (None, bias_begin.numel() - 1):
                 raise TypeError("bias_begin must have one entry more than there are rows")
             n = bias_begin.numel() - 1
-        at += [_given(bias_begin, i32, "bias_begin", like),
-               _given(bias_tokens, i32, "bias_tokens", like, (n_bias,)),
-               _given(bias_values, f32, "bias_values", like, (n_bias,))]
+        at += [_given(bias_begin, i32, "bias_begin", dev),
+               _given(bias_tokens, i32, "bias_tokens", dev, (n_bias,)),
+               _given(bias_values, f32, "bias_values", dev, (n_bias,))]
         n_masks = 0
         if mask is not None:
             if mask.dim() != 2:
@@ -499,12 +513,12 @@ class LogitRules:
         self.rows, self.n_masks = n, n_masks
         self.words = None if mask is None else mask.shape[1]
         self.index_shape = None if mask_index is None else tuple(mask_index.shape)
-        self.history, self.device = history, None if like is None else like.device
+        self.history, self.dev = history, dev
         self._keep = (slots, repetition, frequency, presence, bias_begin, bias_tokens,
                       bias_values, mask, mask_index)
         self.desc = _Rules(None if history is None else ctypes.pointer(history.desc), *at, n_bias,
-                           _given(mask, i32, "mask", like), n_masks,
-                           _given(mask_index, i32, "mask_index", like))
+                           _given(mask, i32, "mask", dev), n_masks,
+                           _given(mask_index, i32, "mask_index", dev))
 
 
 class W4Weight:
@@ -516,26 +530,27 @@ class W4Weight:
         V, H, G = codes.shape[0], 2 * codes.shape[1], scale.shape[1]
         if G < 1 or H % G:
             raise TypeError("scale must be [V, H / group] for codes [V, H / 2]")
-        at = (_given(codes, torch.uint8, "codes", codes),
+        dev = codes.get_device()
+        at = (_given(codes, torch.uint8, "codes", dev),
               _given(scale, torch.float32 if scale.dtype == torch.float32 else torch.bfloat16,
-                     "scale", codes, (V, G)),
-              _given(zero, torch.uint8, "zero", codes, (V, G)))
+                     "scale", dev, (V, G)),
+              _given(zero, torch.uint8, "zero", dev, (V, G)))
         self.codes, self.scale, self.zero = codes, scale, zero
-        self.V, self.H, self.group = V, H, H // G
+        self.V, self.H, self.group, self.dev = V, H, H // G, dev
         self.desc = _W4(*at, SV_F32 if scale.dtype == torch.float32 else SV_BF16, V, H, H // G)
 
 
 def sv_history_reset(history: TokenHistory, slots=None, n: Optional[int] = None, status=None,
                      stream=None) -> None:
     """Empty the listed slots, or the first n (default: all)."""
-    like = history.output_counts
+    dev = history.dev
     if slots is not None:
         n = slots.numel()
     elif n is None:
         n = history.R
-    _call("sv_history_reset", like, stream, history.desc,
-          _given(slots, torch.int32, "slots", like), int(n),
-          _given(status, torch.int32, "status", like))
+    _call("sv_history_reset", dev, stream, history.desc,
+          _given(slots, torch.int32, "slots", dev), int(n),
+          _given(status, torch.int32, "status", dev))
 
 
 def sv_history_add(history: TokenHistory, tokens, lens=None, kind: int = SV_HISTORY_OUTPUT,
@@ -543,13 +558,12 @@ def sv_history_add(history: TokenHistory, tokens, lens=None, kind: int = SV_HIST
     """Append the first lens[b] + extra (default: all) tokens of each row of
     tokens [B, S]; sv_verify's results go in as tokens = out_tokens,
     lens = out_accept_len, extra = 1."""
-    like = history.output_counts
-    B, S = tokens.shape
-    _call("sv_history_add", like, stream, history.desc,
-          _given(slots, torch.int32, "slots", like, (B,)), B,
-          _given(tokens, torch.int32, "tokens", like), S,
-          _given(lens, torch.int32, "lens", like, (B,)), int(extra), int(kind),
-          _given(status, torch.int32, "status", like))
+    dev, (B, S) = history.dev, tokens.shape
+    _call("sv_history_add", dev, stream, history.desc,
+          _given(slots, torch.int32, "slots", dev, (B,)), B,
+          _given(tokens, torch.int32, "tokens", dev), S,
+          _given(lens, torch.int32, "lens", dev, (B,)), extra, kind,
+          _given(status, torch.int32, "status", dev))
 
 
 def sv_logits_process(logits, out, rules: LogitRules, draft_tokens=None, lengths=None,
@@ -557,28 +571,29 @@ def sv_logits_process(logits, out, rules: LogitRules, draft_tokens=None, lengths
                       status=None, stream=None) -> None:
     """Apply `rules` to logits [B, P, Vs] into `out` (which may be `logits`);
     V and v0 place a vocabulary slice (default: the whole vocabulary)."""
-    B, P, Vs = logits.shape
+    dev, (B, P, Vs) = logits.get_device(), logits.shape
     dt = _dtype(logits)
     V = Vs if V is None else int(V)
-    if rules.device is not None and rules.device != logits.device:
-        raise TypeError(f"the rules must be on {logits.device}, are on {rules.device}")
-    if rules.rows not in (None, B):
+    if rules.dev is not None and rules.dev != dev:
+        raise TypeError(f"the rules must be on {logits.device}")
+    if rules.rows is not None and rules.rows != B:
         raise TypeError(f"the rules are for {rules.rows} rows, the logits have {B}")
-    if rules.words not in (None, (V + 31) // 32):
+    if rules.words is not None and rules.words != (V + 31) // 32:
         raise TypeError(f"mask must have {(V + 31) // 32} words a row, has {rules.words}")
-    if rules.index_shape not in (None, (B, P)):
+    if rules.index_shape is not None and rules.index_shape != (B, P):
         raise TypeError(f"mask_index must be [{B}, {P}], is {list(rules.index_shape)}")
     K = 0
     if draft_tokens is not None:
         if draft_tokens.dim() != 2 or draft_tokens.shape[0] != B:
             raise TypeError("draft_tokens must be [B, K]")
         K = draft_tokens.shape[1]
-    _call("sv_logits_process", logits, stream,
-          _given(logits, logits.dtype, "logits", logits),
-          _given(out, logits.dtype, "out", logits, (B, P, Vs)), dt, B, P, V, int(v0), Vs,
-          _given(draft_tokens, torch.int32, "draft_tokens", logits), K, int(pos0),
-          _given(lengths, torch.int32, "lengths", logits, (B,)), int(extra), rules.desc,
-          _given(status, torch.int32, "status", logits))
+    at = _given(logits, logits.dtype, "logits", dev)
+    _call("sv_logits_process", dev, stream, at,
+          at if out is logits else _given(out, logits.dtype, "out", dev, (B, P, Vs)),
+          dt, B, P, V, v0, Vs,
+          _given(draft_tokens, torch.int32, "draft_tokens", dev), K, pos0,
+          _given(lengths, torch.int32, "lengths", dev, (B,)), extra, rules.desc,
+          _given(status, torch.int32, "status", dev))
 
 
 def sv_head_w4_workspace_bytes(weight: W4Weight, B: int, P: int) -> int:
@@ -589,17 +604,17 @@ def sv_head_w4(weight: W4Weight, x, out, workspace=None, lengths=None, extra: in
                stream=None) -> None:
     """out [B, P, V] (float32 or bfloat16) = x [B, P, H] (bfloat16) times the
     4-bit weights; positions p >= lengths[b] + extra are left as they were."""
-    B, P, H = x.shape
+    dev, (B, P, H) = x.get_device(), x.shape
     if H != weight.H:
         raise TypeError(f"x must be [B, P, {weight.H}]")
-    if weight.codes.device != x.device:
-        raise TypeError(f"the weights must be on {x.device}, are on {weight.codes.device}")
-    _call("sv_head_w4", x, stream, weight.desc, _given(x, torch.bfloat16, "x", x), B, P,
-          _given(lengths, torch.int32, "lengths", x, (B,)), int(extra),
-          _given(out, out.dtype, "out", x, (B, P, weight.V)), _dtype(out),
-          None if workspace is None else _given(workspace, workspace.dtype, "workspace", x),
+    if weight.dev != dev:
+        raise TypeError(f"the weights must be on {x.device}")
+    _call("sv_head_w4", dev, stream, weight.desc, _given(x, torch.bfloat16, "x", dev), B, P,
+          _given(lengths, torch.int32, "lengths", dev, (B,)), extra,
+          _given(out, out.dtype, "out", dev, (B, P, weight.V)), _dtype(out),
+          None if workspace is None else _given(workspace, workspace.dtype, "workspace", dev),
           0 if workspace is None else workspace.numel() * workspace.element_size(),
-          _given(status, torch.int32, "status", x))
+          _given(status, torch.int32, "status", dev))
 
 
 def sv_philox_uniforms(seed: int, row, pos, draw, out, stream=None) -> None:

@@ -217,8 +217,8 @@ __device__ __forceinline__ void forbid(const RuleArgs &a, const RuleSmem<true> &
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const char *row = a.out + static_cast<long long>(b) * a.P * a.Vs * ESIZE;
     const long long vec = static_cast<long long>(a.Vs) * ESIZE;
-    constexpr int kSpans = RuleCfg<true>::kChunk / kPer / kSpan + 1;
-    for (int span = warp; span < kSpans; span += RuleCfg<true>::kThreads / 32) {
+    const int spans = (n / kPer + kSpan - 1) / kSpan;    // at most, whatever the alignment
+    for (int span = warp; span < spans; span += RuleCfg<true>::kThreads / 32) {
         for (int p0 = 0; p0 < np; p0 += kAhead) {
             uint32_t w[kAhead];
 #pragma unroll
