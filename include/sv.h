@@ -709,12 +709,15 @@ typedef struct {
  *   workspace      device scratch of sv_head_w4_workspace_bytes(weight, B, P)
  *                  bytes, 16-byte aligned: the scheduled tokens of x in the
  *                  matrix unit's layout.  Calls that share a workspace must
- *                  be stream-ordered.
+ *                  be stream-ordered.  NULL where that is 0 bytes: up to 16
+ *                  tokens (B * P), unless V < 32 or B * P * H is too large
+ *                  for x to be held on chip, take one launch without it.
  *   status         device int32, nullable; SV_NOTE_TIMEOUT is OR-ed in if an
  *                  internal wait ran out (out is then undefined).
  * The same inputs give the same bits on every call.  Never synchronises.
  * Returns SV_OK, SV_ERR_ARG, SV_ERR_SHAPE, SV_ERR_DTYPE, SV_ERR_WORKSPACE or
- * SV_ERR_CUDA.  sv_head_w4_workspace_bytes returns 0 for unsupported sizes.
+ * SV_ERR_CUDA.  sv_head_w4_workspace_bytes also returns 0 for unsupported
+ * sizes.
  */
 size_t sv_head_w4_workspace_bytes(const sv_w4 *weight, int B, int P);
 sv_status sv_head_w4(const sv_w4 *weight, const void *x, int B, int P, const int32_t *lengths,

@@ -1207,9 +1207,6 @@ extern "C" sv_status sv_head_w4(const sv_w4 *weight, const void *x, int B, int P
     a.nh_max = sv::nh_for(M);
     a.ak = sv::ak_for(a.nh_max);
     a.nkb = (a.H + a.ak - 1) / a.ak;
-    CUtensorMap map;
-    cudaError_t e = sv::code_map(weight, a.ak, &map);
-    if (e != cudaSuccess) return sv::note_cuda(e);
     char *w = static_cast<char *>(workspace);
     a.count = reinterpret_cast<int *>(w);
     a.rows = reinterpret_cast<int *>(w + p.off_rows);
@@ -1217,7 +1214,12 @@ extern "C" sv_status sv_head_w4(const sv_w4 *weight, const void *x, int B, int P
     a.status = status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int packs = M < sv::kPackGrid ? M : sv::kPackGrid;
-    e = sv::launch_pdl(sv::pack_kernel, dim3(packs), dim3(sv::kPackThreads), 0, st, a);
+    cudaError_t e = sv::launch_pdl(sv::pack_kernel, dim3(packs), dim3(sv::kPackThreads), 0, st, a);
+    if (e != cudaSuccess) return sv::note_cuda(e);
+    // After a launch, which makes the device's context this thread's: the
+    // driver's call needs one, and a new host thread has none.
+    CUtensorMap map;
+    e = sv::code_map(weight, a.ak, &map);
     if (e != cudaSuccess) return sv::note_cuda(e);
     switch (a.nh_max) {
     case 64: e = sv::launch_group<64>(a, map, st); break;

@@ -71,11 +71,6 @@ __device__ __forceinline__ uint32_t bits32(const uint32_t *plane, int W, int v) 
     return __funnelshift_r(lo, hi, s);
 }
 
-template <int ESIZE> __device__ __forceinline__ float ld_logit(const char *p) {
-    if (ESIZE == 4) return *reinterpret_cast<const float *>(p);
-    return __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const unsigned short *>(p)) << 16);
-}
-
 // The bits of a logit, to be widened once every load of a batch is out: a
 // conversion right behind its load would wait for it.
 template <int ESIZE> __device__ __forceinline__ uint32_t ld_raw(const char *p) {

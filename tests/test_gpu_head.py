@@ -1,5 +1,7 @@
 """The 4-bit output head on the GPU against its plain 64-bit form, and the
 chain head -> rules -> verification -> history."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -161,6 +163,64 @@ def test_head_on_streams_and_in_a_graph():
             torch.cuda.synchronize()
             for i in range(2):
                 plain.check(outs[i].double().cpu().numpy(), *want[i])
+
+
+def test_head_from_two_host_threads():
+    # threads that have made no CUDA call before, one stream each
+    h = Head(512, 2000, 64, True, "bfloat16", seed=13)
+    for M in (9, 20, 140):
+        xs = [h.x(M, 1) for _ in range(2)]
+        outs = [torch.zeros(M, 1, 2000, device="cuda") for _ in xs]
+        need = sv.sv_head_w4_workspace_bytes(h.weight, M, 1)
+        ws = [torch.empty(max(need, 16), dtype=torch.uint8, device="cuda") for _ in xs]
+        streams = [torch.cuda.Stream().cuda_stream for _ in xs]
+        torch.cuda.synchronize()
+        failed = []
+
+        def call(i):
+            try:
+                for _ in range(5):
+                    sv.sv_head_w4(h.weight, xs[i], outs[i], ws[i], stream=streams[i])
+            except Exception as e:
+                failed.append(e)
+
+        threads = [threading.Thread(target=call, args=(i,)) for i in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        torch.cuda.synchronize()
+        assert not failed
+        for i in range(2):
+            plain.check(outs[i].double().cpu().numpy(), *h.want(xs[i], "float32"))
+
+
+@pytest.mark.parametrize("B,P", [(6, 2), (30, 3)])
+def test_head_lengths_at_the_ends_of_their_type(B, P):
+    h = Head(128, 100, 32, False, "float32", seed=17)
+    x, ends = h.x(B, P), torch.tensor([2**31 - 1, -2**31, 0, 1, -1, P], dtype=torch.int32)
+    lengths = ends.repeat(B // 6).cuda()
+    for extra in (0, 1, 2**31 - 1, -2**31):
+        want, bound = h.want(x, "float32")
+        for b, n in enumerate(lengths.tolist()):
+            want[b, max(0, n + extra):], bound[b, max(0, n + extra):] = 55.0, 0.0
+        got = h.run(x, "float32", lengths, extra).double().cpu().numpy()
+        plain.check(got, want, bound)
+
+
+def test_head_most_tokens():
+    # 2^20 positions, the most of a call, and one fewer scheduled
+    h = Head(32, 33, 32, False, "float32", seed=19)
+    x = torch.randint(-3, 4, (1 << 17, 8, 32), dtype=torch.int8, device="cuda").bfloat16()
+    lengths = torch.full((1 << 17,), 8, dtype=torch.int32, device="cuda")
+    lengths[5] = 7
+    got = h.run(x, "float32", lengths)
+    w = torch.from_numpy((h.codes.astype(np.float64) - 8)).cuda() * h.scale.double().cuda()
+    want = x.double() @ w.T
+    # integers of at most 32 * 3 * 8 are exact; the scale's product rounds once
+    bound = want.abs() * 2.0 ** -24
+    want[5, 7], bound[5, 7] = 55.0, 0.0
+    assert bool(((got.double() - want).abs() <= bound).all())
 
 
 def test_head_refuses_a_short_workspace():

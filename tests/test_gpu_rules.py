@@ -269,6 +269,26 @@ def test_rules_one_by_one(kw):
             c.check(in_place, want=want)
 
 
+def test_rows_that_share_a_slot():
+    c = Case(5, 3, 2000, "bfloat16", seed=29, slots=True)
+    c.slots[:] = [4, 1, 4, 4, 1]
+    want = c.want()
+    for in_place in (True, False):
+        c.check(in_place, want=want)
+
+
+@pytest.mark.parametrize("extra", [0, 1, 2**31 - 1, -2**31])
+def test_rules_lengths_at_the_ends_of_their_type(extra):
+    lengths = np.array([2**31 - 1, -2**31, 0, 1, -1, 3], np.int64)
+    c = Case(6, 4, 700, "float32", seed=31, lengths=lengths.astype(np.int32), extra=extra)
+    c.lengths = lengths
+    want = c.want()
+    c.lengths = lengths.astype(np.int32)
+    c.n_pos = lambda b: int(np.clip(int(lengths[b]) + extra, 0, 4))
+    for in_place in (True, False):
+        c.check(in_place, want=want)
+
+
 @pytest.mark.parametrize("v0,Vs", [(0, 1), (0, 10001), (5, 8192), (33, 9000), (8191, 1811),
                                    (10001, 1), (64, 64)])
 def test_rules_on_a_vocabulary_slice(v0, Vs):
