@@ -21,7 +21,7 @@ DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("sv_device.cuh", "sv_host.h")]
     [os.path.join(INCLUDE, "sv.h")]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
-         "-Xcompiler", "-fPIC", "-shared", "-cudart", "static", "-I" + INCLUDE, "-I" + CSRC]
+         "--threads", "0", "-Xcompiler", "-fPIC", "-shared", "-cudart", "static", "-I" + INCLUDE, "-I" + CSRC]
 
 
 def up_to_date() -> bool:
