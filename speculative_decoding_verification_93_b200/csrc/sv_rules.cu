@@ -12,13 +12,22 @@
 //   B. in place, 16-byte units of the masked positions: units a mask forbids
 //      whole are overwritten without being read, mixed ones written element by
 //      element; with a separate output every unit is copied, masked on the way;
-//   C. the touched tokens, one (token, position) a thread: logit, mask word
-//      and count are requested together, the penalised logit is written.  With
-//      a separate output this follows each position's copy, while its lines
-//      are still in the caches.  (Penalising inside the copy was slower, 66
-//      against 59 us at 64 x 5 x 129280 bf16: a few lanes of a warp had work.)
-//   D. the chunk's biased tokens, one (entry, position) a thread.
+//   C. the touched tokens: in place a thread takes up to four positions of a
+//      token, whose logits and mask words are requested together with the
+//      token's count; with a separate output a (token, position) each, after
+//      that position's copy, while its lines are still in the caches.
+//      (Penalising inside the copy was slower, 66 against 59 us at
+//      64 x 5 x 129280 bf16: a few lanes of a warp had work.)
+//   D. the chunk's biased tokens, in place as further items of C.
 // In place, B and C/D touch disjoint elements (forbidden, allowed).
+//
+// Measured, bf16, 256 x 9 x 129280 in place, 1214 positions scheduled, 1.9 M
+// touched logits, a quarter of the rows masked: 74 us.  The touched logits lie
+// alone in their 32-byte sectors and memory moves 64 bytes at a time, so what
+// the DRAM moves (181 MB by its counters), not the 66 MB the rules name, bounds
+// it: penalties alone take 39 us, masks alone 30.  64 x 5 x 129280 with a
+// separate output: 53 us, 36 of them the copy (165 MB); 128 x 17 x 129280
+// fp32, half of it scheduled: 242 us, 195 of them the copy (1.2 GB, 6.1 TB/s).
 #include <climits>
 #include <cstdint>
 
@@ -32,7 +41,9 @@ constexpr int kBiasList = 256;
 
 // In place a CTA mostly waits (for its row's parameters, its planes, then a few
 // logits each), so it takes many tokens; a copy is bound by its bytes, and small
-// CTAs keep more of them on their way.
+// CTAs keep more of them on their way.  In place, at the size below: chunks of
+// 4096 tokens 91 us, 128 threads a CTA 93, 512 threads 112, 8192 tokens and 256
+// threads 74; chunks that grow with the token id 79.
 template <bool IN_PLACE> struct RuleCfg {
     static constexpr int kThreads = IN_PLACE ? 256 : 128;
     static constexpr int kPlane = IN_PLACE ? kThreads : kThreads / 2;   // words of a plane
@@ -302,6 +313,14 @@ __device__ __forceinline__ void copy_position(const RuleArgs &a, int b, int p, i
 
 __device__ __forceinline__ bool valid_bias(float v) { return !isnan(v) && !(isinf(v) && v > 0.f); }
 
+// The token of bias entry e has another before e1, which counts in its place.
+__device__ __forceinline__ bool listed_again(const RuleArgs &a, int e, int e1) {
+    const int t = __ldg(a.bias_tokens + e);
+    for (int f = e + 1; f < e1; ++f)
+        if (__ldg(a.bias_tokens + f) == t && valid_bias(__ldg(a.bias_values + f))) return true;
+    return false;
+}
+
 // Status: the row's parameters, and masks of its first np positions that allow
 // nothing (a row's CTAs share them).
 template <bool IN_PLACE>
@@ -325,7 +344,8 @@ __global__ void __launch_bounds__(RuleCfg<IN_PLACE>::kThreads, RuleCfg<IN_PLACE>
     using Cfg = RuleCfg<IN_PLACE>;
     __shared__ RuleSmem<IN_PLACE> sm;
     constexpr int kThreads = Cfg::kThreads;
-    constexpr int kTokens = 2;           // touched tokens on their way at a time
+    constexpr int kTokens = 2;           // touched tokens on their way at a time (copy)
+    constexpr int kPositions = 4;        // positions of a touched token on their way at a time (in place)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // Rows fastest: the low chunks, where most of a text's tokens lie, first.
     const int chunk = blockIdx.x / a.B, b = blockIdx.x - chunk * a.B;
@@ -333,7 +353,15 @@ __global__ void __launch_bounds__(RuleCfg<IN_PLACE>::kThreads, RuleCfg<IN_PLACE>
     griddep_wait();
     griddep_launch_dependents();
 
-    // Everything about the row in one round trip.
+    // Everything about the row in one round trip, its planes too where its slot
+    // needs no lookup.
+    uint32_t wp = 0, wo = 0;
+    auto planes = [&](int slot) {
+        const long long row = static_cast<long long>(slot) * a.W;
+        wo = bits32(a.output + row, a.W, a.v0 + c0 + 32 * tid);
+        wp = bits32(a.prompt + row, a.W, a.v0 + c0 + 32 * tid);
+    };
+    if (a.prompt && !a.slots && 32 * tid < n) planes(b);
     const int len = a.lengths ? __ldg(a.lengths + b) : 0;
     RowRules r;
     int bits = row_rules(a, b, &r);
@@ -364,15 +392,8 @@ __global__ void __launch_bounds__(RuleCfg<IN_PLACE>::kThreads, RuleCfg<IN_PLACE>
     if (tid <= SV_MAX_K) sm.mask[tid] = m;
     if (tid == 0) sm.dup = sm.nbias = 0;
     for (int w = tid; w < Cfg::kPlane; w += kThreads) sm.draft[w] = sm.bias[w] = 0;
-    // The planes, and the bias list's first entries, are on their way over the
-    // barrier.
-    uint32_t wp = 0, wo = 0;
-    if (penal && r.slot >= 0 && 32 * tid < n) {
-        const uint32_t live = n - 32 * tid >= 32 ? ~0u : (1u << (n - 32 * tid)) - 1u;
-        const long long row = static_cast<long long>(r.slot) * a.W;
-        wo = bits32(a.output + row, a.W, a.v0 + c0 + 32 * tid) & live;
-        if (r.rep != 1.f) wp = bits32(a.prompt + row, a.W, a.v0 + c0 + 32 * tid) & live;
-    }
+    // The bias list's first entries are on their way over the barrier.
+    if (penal && a.slots && r.slot >= 0 && 32 * tid < n) planes(r.slot);
     int bt = -1;
     float bv = 0.f;
     if (e0 + tid < e1) {
@@ -412,6 +433,9 @@ __global__ void __launch_bounds__(RuleCfg<IN_PLACE>::kThreads, RuleCfg<IN_PLACE>
             sm.bvalue[i] = bv;
         }
     }
+    const uint32_t live = !penal || n <= 32 * tid ? 0u : n - 32 * tid >= 32 ? ~0u : (1u << (n - 32 * tid)) - 1u;
+    wo &= live;
+    wp &= r.rep != 1.f ? live : 0u;
     if (tid < Cfg::kPlane) {
         sm.prompt[tid] = wp;
         sm.output[tid] = wo;
@@ -476,37 +500,46 @@ __global__ void __launch_bounds__(RuleCfg<IN_PLACE>::kThreads, RuleCfg<IN_PLACE>
     } else {
         // C. Tokens fastest.  A forbidden logit is read too: waiting for its
         // mask first would cost a second round trip.
-        if (ntouched > 0) {
-            const int dq = kThreads / ntouched, dr = kThreads % ntouched;
-            int q = tid % ntouched, p = tid / ntouched;
-            while (p < np) {
-                uint32_t z[kTokens], word[kTokens];
-                int lv[kTokens], at_p[kTokens], c[kTokens];
+        // The biased tokens (D) come behind the touched ones in the same order,
+        // so that theirs is not a round trip of its own.
+        const int items = ntouched + (sm.nbias <= kBiasList ? sm.nbias : 0);
+        if (items > 0) {
+            const int units = (np + kPositions - 1) / kPositions;    // positions u, u + units, ... a thread
+            const int dq = kThreads / items, dr = kThreads % items;
+            int q = tid % items, u = tid / items;
+            while (u < units) {
+                const int bias = q - ntouched, lv = bias < 0 ? sm.list[q] : sm.btoken[bias];
+                const long long at = row_at + lv * ESIZE;
+                const int t = a.v0 + c0 + lv;
+                uint32_t z[kPositions], word[kPositions];
 #pragma unroll
-                for (int k = 0; k < kTokens; ++k) {
-                    at_p[k] = p;
-                    lv[k] = sm.list[q];
+                for (int k = 0; k < kPositions; ++k) {
+                    const int p = u + k * units;
                     word[k] = ~0u;
                     if (p < np) {
-                        z[k] = ld_raw<ESIZE>(a.in + row_at + p * vec + lv[k] * ESIZE);
-                        c[k] = output_count(a, r, sm, c0, lv[k]);
+                        z[k] = ld_raw<ESIZE>(a.in + at + p * vec);
                         if (masked)
-                            if (const uint32_t *mask = mask_row(a, sm.mask[p])) word[k] = __ldg(mask + ((a.v0 + c0 + lv[k]) >> 5));
+                            if (const uint32_t *mask = mask_row(a, sm.mask[p])) word[k] = __ldg(mask + (t >> 5));
                     }
-                    q += dr;
-                    p += dq;
-                    if (q >= ntouched) { q -= ntouched; ++p; }
                 }
+                const int c = output_count(a, r, sm, c0, lv);
+                const bool replaced = bias >= 0 && sm.dup && listed_again(a, sm.blist[bias], e1);
 #pragma unroll
-                for (int k = 0; k < kTokens; ++k)
-                    if (at_p[k] < np && (word[k] >> ((a.v0 + c0 + lv[k]) & 31) & 1u))
-                        st_logit<ESIZE>(a.out + row_at + at_p[k] * vec + lv[k] * ESIZE,
-                                        penalise(a, r, sm, lv[k], c[k], at_p[k], ndraft, widen<ESIZE>(z[k])));
+                for (int k = 0; k < kPositions; ++k) {
+                    const int p = u + k * units;
+                    if (p >= np || !(word[k] >> (t & 31) & 1u) || replaced) continue;
+                    float y = penalise(a, r, sm, lv, c, p, ndraft, widen<ESIZE>(z[k]));
+                    if (bias >= 0) y += sm.bvalue[bias];
+                    st_logit<ESIZE>(a.out + at + p * vec, y);
+                }
+                q += dr;
+                u += dq;
+                if (q >= items) { q -= items; ++u; }
             }
         }
     }
     // D. Biased tokens: the last entry of a token counts.
-    if (sm.nbias > 0) {
+    if (sm.nbias > (IN_PLACE ? kBiasList : 0)) {
         const bool listed = sm.nbias <= kBiasList;
         const long long pairs = static_cast<long long>(listed ? sm.nbias : e1 - e0) * np;
         for (long long q = tid; q < pairs; q += kThreads) {
@@ -524,12 +557,7 @@ __global__ void __launch_bounds__(RuleCfg<IN_PLACE>::kThreads, RuleCfg<IN_PLACE>
                 if (t < 0 || t >= a.V || lv < 0 || lv >= n || !valid_bias(v)) continue;
             }
             const int t = a.v0 + c0 + lv;
-            if (sm.dup) {
-                bool later = false;
-                for (int f = e + 1; f < e1 && !later; ++f)
-                    later = __ldg(a.bias_tokens + f) == t && valid_bias(__ldg(a.bias_values + f));
-                if (later) continue;
-            }
+            if (sm.dup && listed_again(a, e, e1)) continue;
             const long long to = row_at + p * vec + lv * ESIZE;
             const uint32_t raw = ld_raw<ESIZE>(a.in + to);
             const int c = penal ? output_count(a, r, sm, c0, lv) : 0;
