@@ -44,22 +44,21 @@ namespace sv {
 // ---------------------------------------------------------------------------
 constexpr int kTileV = 128;              // vocabulary rows per tile
 
-// Tokens are taken in `passes` of `per` tokens, each pass in `halves` of `nh`
-// (a multiple of 16) tokens.  The x image of (pass, stage) holds, per half,
+// Tokens are taken in `passes` of `per` tokens, each pass in one or two
+// `halves` of `nh` (a multiple of 16) tokens.  The x image of (pass, stage) holds, per half,
 // blocks of nh rows x 64 k in the 128-byte swizzle.
 struct TokenPlan {
-    int count, passes, per, halves, nh;
+    int count, passes, per, nh;
 };
 
-__host__ __device__ __forceinline__ TokenPlan token_plan(int count, int nh_max) {
+__host__ __device__ __forceinline__ TokenPlan token_plan(int count, int halves, int nh_max) {
     TokenPlan p;
     p.count = count;
-    const int most = 2 * nh_max;
+    const int most = halves * nh_max, unit = 16 * halves;
     p.passes = (count + most - 1) / most;
-    const int share = p.passes ? (count + p.passes - 1) / p.passes : 0;
-    p.halves = share <= 16 ? 1 : 2;
-    p.nh = p.halves == 1 ? 16 : (share + 31) / 32 * 16;
-    p.per = p.halves * p.nh;
+    const int share = p.passes ? (count + p.passes - 1) / p.passes : 1;
+    p.per = (share + unit - 1) / unit * unit;
+    p.nh = p.per / halves;
     return p;
 }
 
@@ -75,7 +74,7 @@ struct HeadArgs {
     const int32_t *lengths;
     int extra;
     void *out;
-    int nh_max;
+    int halves, nh_max;
     int *count;          // workspace: scheduled tokens
     int *rows;           // workspace [B * P]: output row of each packed token
     char *image;         // workspace: x images
@@ -137,7 +136,7 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(HeadArgs a) {
         run += all;
         __syncthreads();
     }
-    const TokenPlan t = token_plan(run, a.nh_max);
+    const TokenPlan t = token_plan(run, a.halves, a.nh_max);
     if (blockIdx.x == 0 && tid == 0) *a.count = run;
     const int chunks = a.H / 8;          // 16-byte chunks of one token
     const int total = mine * chunks;
@@ -292,26 +291,28 @@ struct ParChunk {
     uint32_t off[kParGroups][kTileV];
 };
 
-// Up to NH tokens a half, for weights in groups of GROUP.  AK k per stage, AS
+// HALVES of up to NH tokens, for weights in groups of GROUP.  AK k per stage, AS
 // A operands in tensor memory (AK / 2 columns each, behind the accumulators),
 // CS and XS stages of codes and x in shared memory, WW warpgroups that widen.
-// A batch is one group of one half; DB batches of a half are in tensor memory
-// at a time.
-//   NH = 64: stages of 256 k, which two warpgroups widen in turn.
+// A batch is one group of one half.  Two halves: an accumulating warpgroup and
+// two batches in tensor memory for each.  One half: the two warpgroups take its
+// batches by turns, four in tensor memory.
+//   NH <= 64: stages of 256 k, which two warpgroups widen in turn.
 //   NH = 96: the matrix unit sets the pace (8 nh cycles for 128 k of both
 //   halves; one warpgroup widens that in about 600), and the accumulators
 //   need the registers of a second one.  384 columns of batches leave A two
 //   stages of 128 k.
-template <int NH, int GROUP> struct HeadCfg {
+template <int HALVES, int NH, int GROUP> struct HeadCfg {
+    static constexpr int kHalves = HALVES, kNh = NH;
     static constexpr int AK = NH <= 64 ? 256 : 128;
     static constexpr int AS = 2;
     static constexpr int WW = NH <= 64 ? 2 : 1;
-    static constexpr int DB = 2;
+    static constexpr int DB = 4 / HALVES;              // batches of a half in tensor memory
     static constexpr int XS = 2;
     static constexpr int CS = NH <= 64 ? 4 : 8;
     static constexpr int kSubs = AK / GROUP;
-    static constexpr int kLoad = NH <= 64 ? 16 : 32;   // columns read back at once (twice that many registers)
-    static constexpr int kACol = 2 * DB * NH;
+    static constexpr int kLoad = HALVES == 2 && NH <= 64 ? 16 : 32;   // columns read back at once
+    static constexpr int kACol = 4 * NH;
     static constexpr int kThreads = 128 * (3 + WW);
     // Registers a thread of the service, widening and accumulating
     // warpgroups: their sum stays within what the CTA was launched with.
@@ -321,12 +322,15 @@ template <int NH, int GROUP> struct HeadCfg {
     static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
     static_assert(kRegs0 + WW * kRegsW + 2 * kRegsA <= (3 + WW) * kLaunchRegs, "register split");
     static constexpr int kCodeBytes = kTileV * AK / 2;
-    static constexpr int kXBytes = 2 * NH * AK * 2;
+    static constexpr int kXBytes = HALVES * NH * AK * 2;
+    // One half: what the accumulating warpgroups hand each other, for two jobs.
+    static constexpr int kSums = HALVES == 1 ? NH / 2 * kTileV : 0;
     // More than half of the SM's shared memory, as two CTAs on one SM would
     // wait for each other's tensor memory.
-    static constexpr int kSmem = 1024 + XS * kXBytes + CS * kCodeBytes +
-                                 kParSlots * static_cast<int>(sizeof(ParChunk));
-    static_assert(kSmem > 120 * 1024 && kSmem <= 227 * 1024 - 1024, "shared memory");
+    static constexpr int kUsed = 1024 + XS * kXBytes + CS * kCodeBytes +
+                                 kParSlots * static_cast<int>(sizeof(ParChunk)) + 4 * kSums * 4;
+    static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
+    static_assert(kSmem <= 227 * 1024 - 1024, "shared memory");
     static_assert(kACol + AS * AK / 2 <= static_cast<int>(kTmemCols), "tensor memory");
     static_assert(XS < kDone && AS < kDone && AS % WW == 0, "rings");
 };
@@ -338,6 +342,7 @@ struct HeadBars {
     uint64_t done[kDone];                // the matrix unit is through a stage: its x and A are free
     uint64_t dfull[4], dempty[4];        // a batch finished; read back
     uint64_t pfull[kParSlots], pempty[kParSlots];
+    uint64_t sums;                       // one half: both warpgroups' sums of a job are in shared memory
     uint32_t tmem;
 };
 
@@ -439,11 +444,11 @@ __device__ bool x_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars
 
 // The matrix unit's instructions (warp 1, all lanes together).  Every
 // stage has all its batches; one past the last group has no products.
-template <typename Cfg, int NH, int GROUP>
+template <typename Cfg, int GROUP>
 __device__ bool mma_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars &bar, const char *xring,
                          uint32_t tmem) {
     const uint32_t nh = warp_value(t.nh), nh8 = nh * 8;
-    const int halves = warp_value(t.halves);
+    constexpr int NH = Cfg::kNh;
     const int stages = warp_value(jobs) * a.nkb, last_subs = (a.H - (a.nkb - 1) * Cfg::AK) / GROUP;
     const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((nh >> 3) << 17) | ((kTileV >> 4) << 24);
     const uint32_t x0 = smem_desc(smem_u32(xring));
@@ -467,10 +472,10 @@ __device__ bool mma_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBa
             const uint32_t d = i % Cfg::DB;
             const uint32_t parity = ((i / Cfg::DB) & 1) ^ 1;
             if (!warp_wait(&bar.dempty[d], parity) ||
-                (halves == 2 && !warp_wait(&bar.dempty[Cfg::DB + d], parity))) { ok = false; break; }
+                (Cfg::kHalves == 2 && !warp_wait(&bar.dempty[Cfg::DB + d], parity))) { ok = false; break; }
             tc_fence_after();
 #pragma unroll 1
-            for (int h = 0; h < halves; ++h) {
+            for (int h = 0; h < Cfg::kHalves; ++h) {
                 const uint32_t acc = tmem + (h * Cfg::DB + d) * NH, xh = xs + h * (Cfg::AK / 64) * nh8;
                 if (j < subs) {
 #pragma unroll
@@ -646,96 +651,138 @@ __device__ bool widen_role(const HeadArgs &a, const TokenPlan &t, int jobs, Head
 __device__ __forceinline__ void store_logit(float *p, float z) { *p = z; }
 __device__ __forceinline__ void store_logit(__nv_bfloat16 *p, float z) { *p = __float2bfloat16_rn(z); }
 
-// One warpgroup per half of the tokens; a thread owns one vocabulary row.
-template <typename Cfg, int NH>
+// Adds a batch's first nh columns at `src` in tensor memory, scaled, to acc;
+// the next columns are on their way while these are added.
+template <typename Cfg>
+__device__ __forceinline__ void add_batch(float (&acc)[Cfg::kNh], uint32_t src, float sc, int nh) {
+    constexpr int L = Cfg::kLoad, N = Cfg::kNh / L, kAhead = Cfg::kHalves == 2 ? 2 : 1;
+    const float2 ss = make_float2(sc, sc);
+    float d[kAhead][L];
+    tmem_ld(src, d[0]);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        if (L * k < nh) {
+            if (kAhead == 1 && k > 0) tmem_ld(src + L * k, d[0]);
+            tc_wait_ld(d[k % kAhead]);
+            if (kAhead == 2 && k + 1 < N && L * (k + 1) < nh) tmem_ld(src + L * (k + 1), d[(k + 1) % kAhead]);
+#pragma unroll
+            for (int n = 0; n < L; n += 2) {
+                float *y = acc + L * k + n;
+                const float2 z = __ffma2_rn(make_float2(d[k % kAhead][n], d[k % kAhead][n + 1]), ss, make_float2(y[0], y[1]));
+                y[0] = z.x;
+                y[1] = z.y;
+            }
+        }
+    }
+}
+
+// Writes N of a row's logits, four neighbouring tokens at a time: those of
+// tokens first + (n / 4) * step + n % 4, of which `live` exist.  One vocabulary
+// row per lane: a warp writes 32 consecutive logits of each token.
+template <int N, int ROWS, typename T>
+__device__ __forceinline__ void write_logits(T *out, int V, const float (&y)[N], const int (&rows)[ROWS], int first,
+                                             int step, int live, bool inside) {
+#pragma unroll
+    for (int n0 = 0; n0 < N; n0 += 4) {
+        const int at = first + n0 / 4 * step;
+        if (at < live) {
+            T *to[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                to[n] = out + static_cast<long long>(__shfl_sync(0xffffffffu, rows[n0 / 4 * step / 32], (at + n) % 32)) * V;
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                if (at + n < live && inside) store_logit(to[n], y[n0 + n]);
+        }
+    }
+}
+
+// A thread owns one vocabulary row: of half h, or with one half of every second
+// group (h, h + 2, ...).
+template <typename Cfg>
 __device__ bool accumulate_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars &bar,
-                                const ParChunk *par, uint32_t tmem, int h) {
+                                const ParChunk *par, float *sums, uint32_t tmem, int h) {
+    constexpr int NH = Cfg::kNh, kRows = (NH + 31) / 32;
+    constexpr bool kWhole = Cfg::kHalves == 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarter = warp & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const int batches = a.nkb * Cfg::kSubs;   // of a job and half; one past the last group has no products
     int i = 0, slot = 0, phase = 0;       // batch; slot and phase of the parameter ring
     for (int job = 0; job < jobs; ++job) {
         const int tile = blockIdx.x + job / t.passes * gridDim.x, pass = job % t.passes;
         const int v = tile * kTileV + quarter * 32 + lane;
-        // Output rows of this half's tokens, 32 to a register across the lanes.
-        const int t0 = pass * t.per + h * t.nh, live = min(t.nh, t.count - t0);
-        int rows[(NH + 31) / 32];
+        // Output rows of these tokens, 32 to a register across the lanes.
+        const int t0 = pass * t.per + (kWhole ? 0 : h * t.nh), live = min(t.nh, t.count - t0);
+        int rows[kRows];
 #pragma unroll
-        for (int n = 0; n < (NH + 31) / 32; ++n)
+        for (int n = 0; n < kRows; ++n)
             rows[n] = 32 * n < live ? __ldg(a.rows + t0 + min(32 * n + lane, live - 1)) : 0;
         float acc[NH];
 #pragma unroll
         for (int n = 0; n < NH; ++n) acc[n] = 0.f;
+        constexpr int kStep = kWhole ? 2 : 1;
 #pragma unroll 1
-        for (int kb = 0; kb < a.nkb; ++kb) {
+        for (int g0 = 0; g0 < a.G; g0 += kParGroups) {
+            // This chunk's scales of the row; those past the last group are not used.
+            if (!warp_wait(&bar.pfull[slot], phase)) return false;
+            const float *scale = &par[slot].scale[kWhole ? h : 0][quarter * 32 + lane];
+            const int n_batch = min(kParGroups, batches - g0);
 #pragma unroll 1
-            for (int j = 0; j < Cfg::kSubs; ++j, ++i) {
-                const int g = kb * Cfg::kSubs + j, db = h * Cfg::DB + i % Cfg::DB;
-                if (g % kParGroups == 0 && g < a.G && !warp_wait(&bar.pfull[slot], phase)) return false;
-                if (!warp_wait(&bar.dfull[db], (i / Cfg::DB) & 1)) return false;
+            for (int j = kWhole ? h : 0; j < n_batch; j += kStep, scale += kStep * kTileV) {
+                const int at = i + j, db = kWhole ? at % Cfg::DB : h * Cfg::DB + at % Cfg::DB;
+                const float sc = *scale;
+                if (!warp_wait(&bar.dfull[db], (at / Cfg::DB) & 1)) return false;
                 tc_fence_after();
-                if (g < a.G) {
-                    const float sc = par[slot].scale[g % kParGroups][quarter * 32 + lane];
-                    const float2 ss = make_float2(sc, sc);
-                    const uint32_t src = lanes + db * NH;
-                    // The next columns are on their way while these are added.
-                    float d[2][Cfg::kLoad];
-                    tmem_ld(src, d[0]);
-#pragma unroll
-                    for (int k = 0; k < NH / Cfg::kLoad; ++k) {
-                        if (Cfg::kLoad * k < t.nh) {
-                            tc_wait_ld(d[k & 1]);
-                            if (k + 1 < NH / Cfg::kLoad && Cfg::kLoad * (k + 1) < t.nh)
-                                tmem_ld(src + Cfg::kLoad * (k + 1), d[(k + 1) & 1]);
-#pragma unroll
-                            for (int n = 0; n < Cfg::kLoad; n += 2) {
-                                float *y = acc + Cfg::kLoad * k + n;
-                                const float2 z = __ffma2_rn(make_float2(d[k & 1][n], d[k & 1][n + 1]), ss,
-                                                            make_float2(y[0], y[1]));
-                                y[0] = z.x;
-                                y[1] = z.y;
-                            }
-                        }
-                    }
-                }
+                if (g0 + j < a.G) add_batch<Cfg>(acc, lanes + db * NH, sc, t.nh);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.dempty[db]);
-                if (g < a.G && ((g + 1) % kParGroups == 0 || g + 1 == a.G)) {
-                    if (lane == 0) mbar_arrive(&bar.pempty[slot]);
-                    if (++slot == kParSlots) { slot = 0; phase ^= 1; }
-                }
             }
+            i += n_batch;
+            if (lane == 0) mbar_arrive(&bar.pempty[slot]);
+            if (++slot == kParSlots) { slot = 0; phase ^= 1; }
         }
-        // One vocabulary row per lane: a warp writes 32 consecutive logits of each token.
-        auto write = [&](auto *out) {
+        const bool inside = v < a.V;
+        const long long vo = v;
+        if constexpr (kWhole) {
+            // Each warpgroup takes every second four tokens of both.  Two
+            // buffers by turns: one is written again after the other's sums
+            // of the job between, which came behind its reads, were seen.
+            // (No branches: code that runs once a job is fetched as it runs,
+            // and straight lines are fetched ahead.)
+            float *buf = sums + (job & 1) * 2 * Cfg::kSums + quarter * 32 + lane;
+            float mine[NH / 2];
 #pragma unroll
-            for (int n0 = 0; n0 < NH; n0 += 4) {
-                if (n0 < live) {
-                    decltype(out) to[4];
-#pragma unroll
-                    for (int n = 0; n < 4; ++n)
-                        to[n] = out + static_cast<long long>(__shfl_sync(0xffffffffu, rows[(n0 + n) / 32], (n0 + n) % 32)) * a.V;
-#pragma unroll
-                    for (int n = 0; n < 4; ++n)
-                        if (n0 + n < live && v < a.V) store_logit(to[n], acc[n0 + n]);
-                }
+            for (int n = 0; n < NH / 2; ++n) {
+                const int c = n / 4 * 8 + n % 4;
+                buf[(1 - h) * Cfg::kSums + n * kTileV] = h ? acc[c] : acc[c + 4];
+                mine[n] = h ? acc[c + 4] : acc[c];
             }
-        };
-        if (a.out_f32) write(static_cast<float *>(a.out) + v);
-        else write(static_cast<__nv_bfloat16 *>(a.out) + v);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.sums);
+            if (!warp_wait(&bar.sums, job & 1)) return false;
+#pragma unroll
+            for (int n = 0; n < NH / 2; ++n) mine[n] += buf[h * Cfg::kSums + n * kTileV];
+            if (a.out_f32) write_logits(static_cast<float *>(a.out) + vo, a.V, mine, rows, 4 * h, 8, live, inside);
+            else write_logits(static_cast<__nv_bfloat16 *>(a.out) + vo, a.V, mine, rows, 4 * h, 8, live, inside);
+        } else {
+            if (a.out_f32) write_logits(static_cast<float *>(a.out) + vo, a.V, acc, rows, 0, 4, live, inside);
+            else write_logits(static_cast<__nv_bfloat16 *>(a.out) + vo, a.V, acc, rows, 0, 4, live, inside);
+        }
     }
     return true;
 }
 
-template <int NH, int GROUP>
-__global__ void __launch_bounds__(HeadCfg<NH, GROUP>::kThreads, 1)
+template <int HALVES, int NH, int GROUP>
+__global__ void __launch_bounds__(HeadCfg<HALVES, NH, GROUP>::kThreads, 1)
 head_kernel(HeadArgs a, const __grid_constant__ CUtensorMap map) {
-    using Cfg = HeadCfg<NH, GROUP>;
+    using Cfg = HeadCfg<HALVES, NH, GROUP>;
     extern __shared__ char dyn[];
     __shared__ HeadBars bar;
     char *xring = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~static_cast<uintptr_t>(1023));
     char *cring = xring + Cfg::XS * Cfg::kXBytes;
     ParChunk *par = reinterpret_cast<ParChunk *>(cring + Cfg::CS * Cfg::kCodeBytes);
+    float *sums = reinterpret_cast<float *>(par + kParSlots);
     const int tid = threadIdx.x, warp = warp_value(tid >> 5), lane = tid & 31, wg = warp >> 2;
     CodeCopy<Cfg> codes(a, &map, bar, cring);
     if (tid == 0) {
@@ -743,7 +790,12 @@ head_kernel(HeadArgs a, const __grid_constant__ CUtensorMap map) {
         for (int i = 0; i < Cfg::XS; ++i) mbar_init(&bar.xfull[i], 1);
         for (int i = 0; i < Cfg::AS; ++i) mbar_init(&bar.afull[i], 4);
         for (int i = 0; i < kDone; ++i) mbar_init(&bar.done[i], 1);
-        for (int i = 0; i < 2 * Cfg::DB; ++i) { mbar_init(&bar.dfull[i], 1); mbar_init(&bar.dempty[i], 4); }
+        for (int i = 0; i < 4; ++i) { mbar_init(&bar.dfull[i], 1); mbar_init(&bar.dempty[i], 4); }
+        for (int i = 0; i < kParSlots; ++i) {
+            mbar_init(&bar.pfull[i], 32);
+            mbar_init(&bar.pempty[i], 8 + (a.zero ? 4 * Cfg::WW : 0));
+        }
+        mbar_init(&bar.sums, 8);
         fence_mbar_init();
         // The codes of the first stages are asked for at once: the pack
         // kernel let this grid launch after its own wait, so whatever ran
@@ -753,14 +805,7 @@ head_kernel(HeadArgs a, const __grid_constant__ CUtensorMap map) {
     if (warp == 1) tmem_alloc(&bar.tmem, kTmemCols);
     griddep_wait();
     griddep_launch_dependents();
-    const TokenPlan t = token_plan(__ldcg(a.count), a.nh_max);
-    if (tid == 32) {
-        for (int i = 0; i < kParSlots; ++i) {
-            mbar_init(&bar.pfull[i], 32);
-            mbar_init(&bar.pempty[i], 4 * t.halves + (a.zero ? 4 * Cfg::WW : 0));
-        }
-        fence_mbar_init();
-    }
+    const TokenPlan t = token_plan(__ldcg(a.count), HALVES, NH);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -774,7 +819,7 @@ head_kernel(HeadArgs a, const __grid_constant__ CUtensorMap map) {
         if (warp == 0) {
             if (lane == 0) ok = codes.run(t, jobs);
         } else if (warp == 1) {
-            ok = mma_role<Cfg, NH, GROUP>(a, t, jobs, bar, xring, tmem);
+            ok = mma_role<Cfg, GROUP>(a, t, jobs, bar, xring, tmem);
         } else if (warp == 2) {
             if (lane == 0) ok = x_role<Cfg>(a, t, jobs, bar, xring);
         } else {
@@ -785,8 +830,7 @@ head_kernel(HeadArgs a, const __grid_constant__ CUtensorMap map) {
         ok = widen_role<Cfg, GROUP>(a, t, jobs, bar, cring, par, tmem, wg - 1);
     } else {
         regs_more<Cfg::kRegsA>();
-        const int h = wg - 1 - Cfg::WW;
-        if (h < t.halves) ok = accumulate_role<Cfg, NH>(a, t, jobs, bar, par, tmem, h);
+        ok = accumulate_role<Cfg>(a, t, jobs, bar, par, sums, tmem, wg - 1 - Cfg::WW);
     }
     if (!ok && a.status) atomicOr(a.status, SV_NOTE_TIMEOUT);
     __syncwarp();
@@ -1094,8 +1138,9 @@ static sv_status head_check(const sv_w4 *w, int B, int P) {
     return SV_OK;
 }
 
-// Tokens per half for a batch of at most M tokens, and k per stage.
-static int nh_for(int M) { return M <= 128 ? 64 : 96; }
+// Halves, tokens of each and k per stage, for a batch of at most M tokens.
+static int halves_for(int M) { return M <= 64 ? 1 : 2; }
+static int nh_for(int M) { return M <= 32 ? 32 : M <= 128 ? 64 : 96; }
 static int ak_for(int nh) { return nh <= 64 ? 256 : 128; }
 
 static bool few(const sv_w4 *w, int M) {
@@ -1113,8 +1158,8 @@ static HeadPlan head_plan(const sv_w4 *w, int B, int P) {
     p.off_rows = 16;
     p.off_image = align(16 + 4ull * M);
     // Whatever the scheduled count is, it packs into at most as many passes
-    // as M does, each of at most 2 nh tokens.
-    const size_t most = 2 * nh, passes = (M + most - 1) / most;
+    // as M does, each of at most that many tokens.
+    const size_t most = halves_for(M) * nh, passes = (M + most - 1) / most;
     p.bytes = p.off_image + passes * most * nkb * ak * 2ull;
     return p;
 }
@@ -1146,26 +1191,26 @@ static cudaError_t code_map(const sv_w4 *w, int ak, CUtensorMap *map) {
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int NH, int GROUP>
+template <int HALVES, int NH, int GROUP>
 static cudaError_t launch_head(const HeadArgs &a, const CUtensorMap &map, cudaStream_t st) {
-    using Cfg = HeadCfg<NH, GROUP>;
+    using Cfg = HeadCfg<HALVES, NH, GROUP>;
     static std::atomic<bool> attr_set[64];
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess && !attr_set[dev & 63].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(head_kernel<NH, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+        e = cudaFuncSetAttribute(head_kernel<HALVES, NH, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
         if (e == cudaSuccess) attr_set[dev & 63].store(true, std::memory_order_release);
     }
     if (e != cudaSuccess) return e;
-    return launch_pdl(head_kernel<NH, GROUP>, dim3(a.tiles < sms ? a.tiles : sms), dim3(Cfg::kThreads), Cfg::kSmem,
+    return launch_pdl(head_kernel<HALVES, NH, GROUP>, dim3(a.tiles < sms ? a.tiles : sms), dim3(Cfg::kThreads), Cfg::kSmem,
                       st, a, map);
 }
 
-template <int NH> static cudaError_t launch_group(const HeadArgs &a, const CUtensorMap &map, cudaStream_t st) {
-    if (a.group == 128) return launch_head<NH, 128>(a, map, st);
-    if (a.group == 64) return launch_head<NH, 64>(a, map, st);
-    return launch_head<NH, 32>(a, map, st);
+template <int HALVES, int NH> static cudaError_t launch_group(const HeadArgs &a, const CUtensorMap &map, cudaStream_t st) {
+    if (a.group == 128) return launch_head<HALVES, NH, 128>(a, map, st);
+    if (a.group == 64) return launch_head<HALVES, NH, 64>(a, map, st);
+    return launch_head<HALVES, NH, 32>(a, map, st);
 }
 
 }  // namespace sv
@@ -1204,6 +1249,7 @@ extern "C" sv_status sv_head_w4(const sv_w4 *weight, const void *x, int B, int P
     const int M = B * P;
     if (few)
         return sv::note_cuda(sv::launch_few_tokens(a, M, static_cast<cudaStream_t>(stream)));
+    a.halves = sv::halves_for(M);
     a.nh_max = sv::nh_for(M);
     a.ak = sv::ak_for(a.nh_max);
     a.nkb = (a.H + a.ak - 1) / a.ak;
@@ -1221,9 +1267,7 @@ extern "C" sv_status sv_head_w4(const sv_w4 *weight, const void *x, int B, int P
     CUtensorMap map;
     e = sv::code_map(weight, a.ak, &map);
     if (e != cudaSuccess) return sv::note_cuda(e);
-    switch (a.nh_max) {
-    case 64: e = sv::launch_group<64>(a, map, st); break;
-    default: e = sv::launch_group<96>(a, map, st); break;
-    }
+    if (a.halves == 1) e = a.nh_max == 32 ? sv::launch_group<1, 32>(a, map, st) : sv::launch_group<1, 64>(a, map, st);
+    else e = a.nh_max == 64 ? sv::launch_group<2, 64>(a, map, st) : sv::launch_group<2, 96>(a, map, st);
     return sv::note_cuda(e);
 }
