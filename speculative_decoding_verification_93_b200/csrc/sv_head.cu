@@ -557,13 +557,14 @@ __device__ bool param_role(const HeadArgs &a, const TokenPlan &t, int jobs, Head
     return true;
 }
 
-// One of WW warpgroups: the stages s = wi mod WW, one weight row a thread, 128 k
-// (a step) at a time.  The next step's codes are read from shared memory while
-// this step's are widened.
+// One of WW warpgroups: the stages s = wi mod WW, one weight row a thread, 32 k
+// (a piece) at a time.  The next piece's codes are read from shared memory while
+// this one's are widened.  Four pieces to a round of the loop (17 tokens of
+// 129280 x 4096, group 128: 89 us; two 93, one 99).
 template <typename Cfg, int GROUP>
 __device__ bool widen_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars &bar, const char *ring,
                            const ParChunk *par, uint32_t tmem, int wi) {
-    constexpr int kRowBytes = Cfg::AK / 2, kSteps = Cfg::AK / 128, kMine = 128 / GROUP;   // groups of a step
+    constexpr int kRowBytes = Cfg::AK / 2, kPieces = Cfg::AK / 32, kEach = GROUP / 32;   // pieces of a stage, a group
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
     const int stages = jobs * a.nkb, chunks = (a.G + kParGroups - 1) / kParGroups;
     const int r = quarter * 32 + lane;
@@ -571,9 +572,7 @@ __device__ bool widen_role(const HeadArgs &a, const TokenPlan &t, int jobs, Head
     const int swz = kRowBytes == 128 ? r & 7 : (r >> 1) & 3;
     const uint32_t dst0 = tmem + Cfg::kACol + (static_cast<uint32_t>(quarter * 32) << 16);
     int kb = wi, c0 = 0, have = -1;       // stage of the job, chunks before the job, chunk at hand
-    uint32_t off[kMine];
-#pragma unroll
-    for (int g = 0; g < kMine; ++g) off[g] = zero_pair(8);
+    uint32_t off = zero_pair(8);
     // Hand back chunk `have`, wait for the next one.
     auto next_chunk = [&](bool wait) {
         if (have >= 0) {
@@ -584,63 +583,56 @@ __device__ bool widen_role(const HeadArgs &a, const TokenPlan &t, int jobs, Head
         ++have;
         return !wait || warp_wait(&bar.pfull[have % kParSlots], (have / kParSlots) & 1);
     };
-    uint4 u[4];                           // the codes of the step at hand
-    auto load = [&](uint4 (&to)[4], int s, int step) {
-        const int slot = s % Cfg::CS;
-        if (step == 0 && !warp_wait(&bar.cfull[slot], (s / Cfg::CS) & 1)) return false;
-        const char *row = ring + slot * Cfg::kCodeBytes + r * kRowBytes;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) to[j] = *reinterpret_cast<const uint4 *>(row + (((4 * step + j) ^ swz) * 16));
+    // Zero point of piece q of the stage at kb.
+    auto zero_of = [&](int q) {
+        const int gi = min(kb * Cfg::kSubs + q / kEach, a.G - 1), c = c0 + gi / kParGroups;
+        while (have < c)
+            if (!next_chunk(true)) return false;
+        off = par[c % kParSlots].off[gi % kParGroups][r];
         return true;
     };
-    if (wi < stages && !load(u, wi, 0)) return false;
+    const char *row = ring + r * kRowBytes;
+    uint4 u;
+    auto first = [&](int s) {             // of stage s
+        if (!warp_wait(&bar.cfull[s % Cfg::CS], (s / Cfg::CS) & 1)) return false;
+        row = ring + s % Cfg::CS * Cfg::kCodeBytes + r * kRowBytes;
+        u = *reinterpret_cast<const uint4 *>(row + swz * 16);
+        while (kb >= a.nkb) { kb -= a.nkb; c0 += chunks; }
+        return !a.zero || zero_of(0);
+    };
+    if (wi < stages && !first(wi)) return false;
 #pragma unroll 1
     for (int s = wi; s < stages; s += Cfg::WW) {
         const int ab = s % Cfg::AS, old = s - Cfg::AS;
-        while (kb >= a.nkb) { kb -= a.nkb; c0 += chunks; }
-#pragma unroll 1
-        for (int step = 0; step < kSteps; ++step) {
-            const bool last = step == kSteps - 1;
-            uint4 next[4] = {u[0], u[1], u[2], u[3]};
-            if (!last || s + Cfg::WW < stages)
-                if (!load(next, last ? s + Cfg::WW : s, last ? 0 : step + 1)) return false;
-            if (a.zero) {
-#pragma unroll
-                for (int g = 0; g < kMine; ++g) {
-                    const int gi = min(kb * Cfg::kSubs + step * kMine + g, a.G - 1), c = c0 + gi / kParGroups;
-                    while (have < c)
-                        if (!next_chunk(true)) return false;
-                    off[g] = par[c % kParSlots].off[gi % kParGroups][r];
-                }
+        const uint32_t dst = dst0 + ab * (Cfg::AK / 2);
+        if (old >= 0 && !warp_wait(&bar.done[old % kDone], (old / kDone) & 1)) return false;
+        tc_fence_after();
+#pragma unroll 4
+        for (int q = 0; q < kPieces; ++q) {
+            const uint4 v = u;
+            const uint32_t o = off;
+            if (q + 1 < kPieces) {
+                u = *reinterpret_cast<const uint4 *>(row + (((q + 1) ^ swz) * 16));
+                if (a.zero && (q + 1) % kEach == 0 && !zero_of(q + 1)) return false;
             }
-            if (step == 0 && old >= 0 && !warp_wait(&bar.done[old % kDone], (old / kDone) & 1)) return false;
-            tc_fence_after();
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t o = off[j * 32 / GROUP];
-                uint32_t w[16];
-                widen8(u[j].x, o, w);
-                widen8(u[j].y, o, w + 4);
-                widen8(u[j].z, o, w + 8);
-                widen8(u[j].w, o, w + 12);
-                tmem_st16(dst0 + ab * (Cfg::AK / 2) + step * 64 + j * 16, w);
-            }
-            if (last) {
-                // A is written, and the stage's codes (all steps) were read
-                // into registers in every lane.
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&bar.afull[ab]);
-                    mbar_arrive(&bar.cempty[s % Cfg::CS]);
-                }
-                __syncwarp();
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) u[j] = next[j];
+            uint32_t w[16];
+            widen8(v.x, o, w);
+            widen8(v.y, o, w + 4);
+            widen8(v.z, o, w + 8);
+            widen8(v.w, o, w + 12);
+            tmem_st16(dst + q * 16, w);
         }
+        // A is written, and the stage's codes were read into registers.
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&bar.afull[ab]);
+            mbar_arrive(&bar.cempty[s % Cfg::CS]);
+        }
+        __syncwarp();
         kb += Cfg::WW;
+        if (s + Cfg::WW < stages && !first(s + Cfg::WW)) return false;
     }
     if (a.zero)
         for (const int all = jobs * chunks; have < all;)
