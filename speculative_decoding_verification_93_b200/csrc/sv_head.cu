@@ -307,12 +307,12 @@ template <int HALVES, int NH, int GROUP> struct HeadCfg {
     static constexpr int AK = NH <= 64 ? 256 : 128;
     static constexpr int AS = 2;
     static constexpr int WW = NH <= 64 ? 2 : 1;
-    static constexpr int DB = 4 / HALVES;              // batches of a half in tensor memory
+    static constexpr int DB = NH == 128 ? 3 : 4 / HALVES;   // batches of a half in tensor memory
     static constexpr int XS = 2;
     static constexpr int CS = NH <= 64 ? 4 : 8;
     static constexpr int kSubs = AK / GROUP;
     static constexpr int kLoad = HALVES == 2 && NH <= 64 ? 16 : 32;   // columns read back at once
-    static constexpr int kACol = 4 * NH;
+    static constexpr int kACol = HALVES * DB * NH;
     static constexpr int kThreads = 128 * (3 + WW);
     // Registers a thread of the service, widening and accumulating
     // warpgroups: their sum stays within what the CTA was launched with.
@@ -323,12 +323,12 @@ template <int HALVES, int NH, int GROUP> struct HeadCfg {
     static_assert(kRegs0 + WW * kRegsW + 2 * kRegsA <= (3 + WW) * kLaunchRegs, "register split");
     static constexpr int kCodeBytes = kTileV * AK / 2;
     static constexpr int kXBytes = HALVES * NH * AK * 2;
-    // One half: what the accumulating warpgroups hand each other, for two jobs.
+    // One half: what the accumulating warpgroups hand each other.
     static constexpr int kSums = HALVES == 1 ? NH / 2 * kTileV : 0;
     // More than half of the SM's shared memory, as two CTAs on one SM would
     // wait for each other's tensor memory.
     static constexpr int kUsed = 1024 + XS * kXBytes + CS * kCodeBytes +
-                                 kParSlots * static_cast<int>(sizeof(ParChunk)) + 4 * kSums * 4;
+                                 kParSlots * static_cast<int>(sizeof(ParChunk)) + 2 * kSums * 4;
     static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
     static_assert(kSmem <= 227 * 1024 - 1024, "shared memory");
     static_assert(kACol + AS * AK / 2 <= static_cast<int>(kTmemCols), "tensor memory");
@@ -342,7 +342,7 @@ struct HeadBars {
     uint64_t done[kDone];                // the matrix unit is through a stage: its x and A are free
     uint64_t dfull[4], dempty[4];        // a batch finished; read back
     uint64_t pfull[kParSlots], pempty[kParSlots];
-    uint64_t sums;                       // one half: both warpgroups' sums of a job are in shared memory
+    uint64_t sums, summed;               // one half: both warpgroups' sums of a job are in shared memory; read
     uint32_t tmem;
 };
 
@@ -737,12 +737,11 @@ __device__ bool accumulate_role(const HeadArgs &a, const TokenPlan &t, int jobs,
         const bool inside = v < a.V;
         const long long vo = v;
         if constexpr (kWhole) {
-            // Each warpgroup takes every second four tokens of both.  Two
-            // buffers by turns: one is written again after the other's sums
-            // of the job between, which came behind its reads, were seen.
-            // (No branches: code that runs once a job is fetched as it runs,
-            // and straight lines are fetched ahead.)
-            float *buf = sums + (job & 1) * 2 * Cfg::kSums + quarter * 32 + lane;
+            // Each warpgroup takes every second four tokens of both.  (No
+            // branches: code that runs once a job is fetched as it runs, and
+            // straight lines are fetched ahead.)
+            float *buf = sums + quarter * 32 + lane;
+            if (job > 0 && !warp_wait(&bar.summed, (job - 1) & 1)) return false;
             float mine[NH / 2];
 #pragma unroll
             for (int n = 0; n < NH / 2; ++n) {
@@ -755,6 +754,8 @@ __device__ bool accumulate_role(const HeadArgs &a, const TokenPlan &t, int jobs,
             if (!warp_wait(&bar.sums, job & 1)) return false;
 #pragma unroll
             for (int n = 0; n < NH / 2; ++n) mine[n] += buf[h * Cfg::kSums + n * kTileV];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.summed);
             if (a.out_f32) write_logits(static_cast<float *>(a.out) + vo, a.V, mine, rows, 4 * h, 8, live, inside);
             else write_logits(static_cast<__nv_bfloat16 *>(a.out) + vo, a.V, mine, rows, 4 * h, 8, live, inside);
         } else {
@@ -788,6 +789,7 @@ head_kernel(HeadArgs a, const __grid_constant__ CUtensorMap map) {
             mbar_init(&bar.pempty[i], 8 + (a.zero ? 4 * Cfg::WW : 0));
         }
         mbar_init(&bar.sums, 8);
+        mbar_init(&bar.summed, 8);
         fence_mbar_init();
         // The codes of the first stages are asked for at once: the pack
         // kernel let this grid launch after its own wait, so whatever ran
@@ -1131,8 +1133,8 @@ static sv_status head_check(const sv_w4 *w, int B, int P) {
 }
 
 // Halves, tokens of each and k per stage, for a batch of at most M tokens.
-static int halves_for(int M) { return M <= 64 ? 1 : 2; }
-static int nh_for(int M) { return M <= 32 ? 32 : M <= 128 ? 64 : 96; }
+static int halves_for(int M) { return M <= 128 ? 1 : 2; }
+static int nh_for(int M) { return M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 96; }
 static int ak_for(int nh) { return nh <= 64 ? 256 : 128; }
 
 static bool few(const sv_w4 *w, int M) {
@@ -1259,7 +1261,11 @@ extern "C" sv_status sv_head_w4(const sv_w4 *weight, const void *x, int B, int P
     CUtensorMap map;
     e = sv::code_map(weight, a.ak, &map);
     if (e != cudaSuccess) return sv::note_cuda(e);
-    if (a.halves == 1) e = a.nh_max == 32 ? sv::launch_group<1, 32>(a, map, st) : sv::launch_group<1, 64>(a, map, st);
-    else e = a.nh_max == 64 ? sv::launch_group<2, 64>(a, map, st) : sv::launch_group<2, 96>(a, map, st);
+    switch (a.nh_max) {
+    case 32: e = sv::launch_group<1, 32>(a, map, st); break;
+    case 64: e = sv::launch_group<1, 64>(a, map, st); break;
+    case 128: e = sv::launch_group<1, 128>(a, map, st); break;
+    default: e = sv::launch_group<2, 96>(a, map, st); break;
+    }
     return sv::note_cuda(e);
 }
