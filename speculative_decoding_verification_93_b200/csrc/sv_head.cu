@@ -11,23 +11,37 @@
 // group's sum is read back from tensor memory, multiplied by its scale in
 // fp32 and added to fp32 accumulators in registers.
 //
-// One launch packs the scheduled tokens of x into the operand layout
-// (pack_kernel); the second (head_kernel) is persistent, one CTA per SM, and
-// walks 128-row tiles of the vocabulary, K in stages of AK (256, or 128 above
-// 128 tokens):
+// Up to 16 tokens take few_kernel (section 4), one launch.  Otherwise one launch
+// packs the scheduled tokens of x into the operand layout (pack_kernel); the
+// second (head_kernel) is persistent, one CTA per SM, and walks 128-row tiles of
+// the vocabulary, K in stages of AK (256, or 128 above 64 tokens):
 //   warp 0      asks for each stage's codes (one TMA tile, swizzled);
 //   warp 2      copies each stage's x image (bulk copies);
 //   warp 3      fetches scales and zero points into a ring of their own;
 //   warp 1      issues tcgen05.mma, A from tensor memory, B from shared
-//               memory, one batch per (groups, half of the tokens);
+//               memory, one batch per group and half of the tokens;
 //   one or two warpgroups own one weight row per thread: they widen codes to
 //               bf16 integers and write them to tensor memory as A;
-//   one or two warpgroups, one per half of the tokens, read each finished
-//               batch back, scale and accumulate it, and write the logits.
-// The two halves alternate, so the matrix unit works on one half while the
-// other is read back.  A in tensor memory keeps the widened weights (four
-// times the bytes of the codes) out of shared memory, whose bandwidth the B
-// operand needs.
+//   two warpgroups read each finished batch back, scale and accumulate it, and
+//               write the logits: up to 128 tokens by turns (every second
+//               group each, the sums added at the end), above that one for
+//               each half of the tokens.
+// A in tensor memory keeps the widened weights (four times the bytes of the
+// codes) out of shared memory, whose bandwidth the B operand needs.
+//
+// Measured, V x H = 129280 x 4096, bf16 out, groups of 128 / 64 / 32 (the last
+// two with zero points):
+//      1 token   57 /  91 / 130 us (273 MB for groups of 128: 4.8 TB/s)
+//      9 tokens  75 / 119 / 153
+//     32 tokens  88 / 120 / 175
+//     64 tokens 102 / 133 / 209
+//    128 tokens 152 / 201 / 276
+//    192 tokens 192 / 231 / 389 (203 GFLOP: 1.06 PFLOP/s for groups of 128)
+// Every group costs a round of hand-overs (products, read-back, buffer free),
+// some 250 cycles whatever its length, and every 128 k a widening warpgroup
+// some 1000: neither memory nor the matrix unit (16 cycles a product at 32
+// tokens, 50 at 96, measured by issuing each twice) sets the pace before 192
+// tokens, where the unit is half busy.
 #include <atomic>
 #include <climits>
 #include <cstdint>
@@ -223,15 +237,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&f)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7]),
-          "=f"(f[8]), "=f"(f[9]), "=f"(f[10]), "=f"(f[11]), "=f"(f[12]), "=f"(f[13]), "=f"(f[14]), "=f"(f[15])
-        : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&f)[32]) {
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&f)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -242,16 +248,8 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&f)[32]) {
           "=f"(f[24]), "=f"(f[25]), "=f"(f[26]), "=f"(f[27]), "=f"(f[28]), "=f"(f[29]), "=f"(f[30]), "=f"(f[31])
         : "r"(addr) : "memory");
 }
-__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&f)[16]) { tmem_ld16(addr, f); }
-__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&f)[32]) { tmem_ld32(addr, f); }
 // Loads from tensor memory land by the wait; naming their registers here
 // keeps every use behind it.
-__device__ __forceinline__ void tc_wait_ld(float (&f)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3]), "+f"(f[4]), "+f"(f[5]), "+f"(f[6]), "+f"(f[7]),
-                   "+f"(f[8]), "+f"(f[9]), "+f"(f[10]), "+f"(f[11]), "+f"(f[12]), "+f"(f[13]), "+f"(f[14]), "+f"(f[15])
-                 :: "memory");
-}
 __device__ __forceinline__ void tc_wait_ld(float (&f)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3]), "+f"(f[4]), "+f"(f[5]), "+f"(f[6]), "+f"(f[7]),
@@ -296,12 +294,13 @@ struct ParChunk {
 // CS and XS stages of codes and x in shared memory, WW warpgroups that widen.
 // A batch is one group of one half.  Two halves: an accumulating warpgroup and
 // two batches in tensor memory for each.  One half: the two warpgroups take its
-// batches by turns, four in tensor memory.
+// batches by turns, four (NH = 128: three) in tensor memory.
 //   NH <= 64: stages of 256 k, which two warpgroups widen in turn.
-//   NH = 96: the matrix unit sets the pace (8 nh cycles for 128 k of both
-//   halves; one warpgroup widens that in about 600), and the accumulators
-//   need the registers of a second one.  384 columns of batches leave A two
-//   stages of 128 k.
+//   NH > 64: the accumulators need the registers of a second widening
+//   warpgroup, and 384 columns of batches leave A two stages of 128 k.
+// One half is the faster form wherever its batches fit (three at least): two
+// halves of 64 took 150 / 213 / 366 us at 128 tokens, two of 16 135 / 217 / 357
+// at 17.
 template <int HALVES, int NH, int GROUP> struct HeadCfg {
     static constexpr int kHalves = HALVES, kNh = NH;
     static constexpr int AK = NH <= 64 ? 256 : 128;
@@ -311,7 +310,6 @@ template <int HALVES, int NH, int GROUP> struct HeadCfg {
     static constexpr int XS = 2;
     static constexpr int CS = NH <= 64 ? 4 : 8;
     static constexpr int kSubs = AK / GROUP;
-    static constexpr int kLoad = HALVES == 2 && NH <= 64 ? 16 : 32;   // columns read back at once
     static constexpr int kACol = HALVES * DB * NH;
     static constexpr int kThreads = 128 * (3 + WW);
     // Registers a thread of the service, widening and accumulating
@@ -647,7 +645,7 @@ __device__ __forceinline__ void store_logit(__nv_bfloat16 *p, float z) { *p = __
 // the next columns are on their way while these are added.
 template <typename Cfg>
 __device__ __forceinline__ void add_batch(float (&acc)[Cfg::kNh], uint32_t src, float sc, int nh) {
-    constexpr int L = Cfg::kLoad, N = Cfg::kNh / L, kAhead = Cfg::kHalves == 2 ? 2 : 1;
+    constexpr int L = 32, N = Cfg::kNh / L, kAhead = Cfg::kHalves == 2 ? 2 : 1;
     const float2 ss = make_float2(sc, sc);
     float d[kAhead][L];
     tmem_ld(src, d[0]);
@@ -838,8 +836,8 @@ head_kernel(HeadArgs a, const __grid_constant__ CUtensorMap map) {
 // 4. Few tokens: one launch, no tensor memory.
 //
 // With at most 16 tokens nothing but the weights' bytes costs, and the
-// hand-overs between roles above would set the pace (measured at one token of
-// 129280 x 4096: 78 us).  Here a warp does all of it for 32 vocabulary rows:
+// hand-overs between roles above would set the pace (17 tokens of 129280 x
+// 4096 take 87 us there).  Here a warp does all of it for 32 vocabulary rows:
 // codes straight into registers, two blocks of 128 k ahead; widened there;
 // multiplied by mma.sync with the rows as M = 16 and the tokens as N = 8 or 16
 // (the matrix unit is idle most of the time, so its older path is enough);
