@@ -909,8 +909,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(HeadArgs a, int spl
     const int per = nkb * 16;
     for (int i = tid; i < count * per; i += kFewThreads) {
         const int tok = i / per, c = i - tok * per;
-        if (c * 8 >= a.H) continue;
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(a.x + static_cast<long long>(rows[tok]) * a.H) + c);
+        uint4 u = make_uint4(0, 0, 0, 0);     // past the end: groups without a share (see live below)
+        if (c * 8 < a.H) u = __ldg(reinterpret_cast<const uint4 *>(a.x + static_cast<long long>(rows[tok]) * a.H) + c);
         uint4 w;
         w.x = __byte_perm(u.x, u.z, 0x5410);
         w.y = __byte_perm(u.x, u.z, 0x7632);
@@ -938,7 +938,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(HeadArgs a, int spl
     // Rows g + 8 r.  Codes on their way; scales and zero points by sets of four
     // groups, of which each lane of a quad holds one: the rows' reads touch a
     // quarter of the lines, and a shuffle hands them on.
-    uint32_t w[kAhead][4][4], sc[kSet][4], zp[kSet][4];
+    uint32_t w[kAhead][4][4] = {}, sc[kSet][4], zp[kSet][4];
     const uint8_t *codes = nullptr;       // next block to fetch, row g
     long long par = 0;                    // index of its first scale, row g
     int f_tile = first, f_kb = lo;
@@ -951,7 +951,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(HeadArgs a, int spl
         if (f_tile >= tiles) return;
 #pragma unroll
         for (int q = 0; q < kSubs; ++q) {
-            if (kSubs > 1 && f_kb * kSubs + q >= a.G) break;
+            if (kSubs == 1 || f_kb * kSubs + q < a.G)
 #pragma unroll
             for (int r = 0; r < 4; ++r) ld_codes<kWords>(w[u][r] + q * kWords, codes + r * 8 * row_bytes + q * (GROUP / 2));
         }
@@ -1035,13 +1035,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(HeadArgs a, int spl
             const int xo = kb * 256;
 #pragma unroll
             for (int q = 0; q < kSubs; ++q) {
-                if (kSubs > 1 && kb * kSubs + q >= a.G) break;
+                // No branch here, so that the groups' products overlap.
+                const bool live = kSubs == 1 || kb * kSubs + q < a.G;
                 const int from = (lane & ~3) + in_set + q;
                 float f[4];
                 uint32_t o[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     f[r] = __uint_as_float(__shfl_sync(0xffffffffu, sc[set][r], from));
+                    if (!live) f[r] = 0.f;
                     o[r] = ZERO ? __shfl_sync(0xffffffffu, zp[set][r], from) : eight;
                 }
                 float part[2][NT][4];
