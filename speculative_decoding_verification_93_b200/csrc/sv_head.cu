@@ -31,8 +31,8 @@
 //
 // Measured, V x H = 129280 x 4096, bf16 out, groups of 128 / 64 / 32 (the last
 // two with zero points):
-//      1 token   57 /  91 / 130 us (273 MB for groups of 128: 4.8 TB/s)
-//      9 tokens  75 / 119 / 153
+//      1 token   57 /  80 / 133 us (273 MB for groups of 128: 4.8 TB/s)
+//      9 tokens  75 / 119 / 154
 //     32 tokens  88 / 120 / 175
 //     64 tokens 102 / 133 / 209
 //    128 tokens 152 / 201 / 276

@@ -5,6 +5,10 @@
 // A slot is two bit planes over the vocabulary (prompt, output) and one count
 // per token.  The planes are what a reader scans (V / 8 bytes instead of 4 V
 // bytes of counts); a count is looked up only where its bit is set.
+//
+// Both kernels are bound by their launch: 64 prompts of up to 4096 tokens take
+// 6.3 us cold under a profiler, and a call takes 5 us back to back, what issuing
+// it from Python costs, whatever its size.
 #include <climits>
 #include <cstdint>
 
