@@ -100,6 +100,14 @@ def test_head_few_tokens_of_a_large_vocabulary(V):
         h.check(h.x(M, 1), "float32")
 
 
+@pytest.mark.parametrize("M", [17, 40, 64, 100, 200])
+@pytest.mark.parametrize("H,group,zero", [(384, 128, False), (128, 128, True), (96, 32, True), (448, 64, False)])
+def test_head_several_tiles_a_block(M, H, group, zero):
+    # three tiles of 128 rows for some blocks; odd and even numbers of groups
+    h = Head(H, 2 * 148 * 128 + 130, group, zero, "bfloat16", seed=M + H)
+    h.check(h.x(M, 1), "bfloat16")
+
+
 @pytest.mark.parametrize("B,P", [(1, 1), (5, 4), (40, 5), (3, 9), (16, 1)])
 def test_head_leaves_unscheduled_positions_as_they_were(B, P):
     h = Head(512, 1031, 128, True, "bfloat16", seed=B)
