@@ -619,7 +619,7 @@ typedef struct {
     const int32_t *bias_begin;   /* device int32 [B+1], nullable (no biases): row b has the */
     const int32_t *bias_tokens;  /*   entries bias_begin[b] .. bias_begin[b+1]-1 of these   */
     const float *bias_values;    /*   two device arrays of n_bias entries                   */
-    int n_bias;
+    int n_bias;                  /*   0 <= n_bias <= 2^30                                   */
     const uint32_t *mask;        /* device [n_masks, W], nullable: bit 1 = token allowed */
     int n_masks;
     const int32_t *mask_index;   /* device int32 [B, P], nullable: the mask of (b, p), -1 for

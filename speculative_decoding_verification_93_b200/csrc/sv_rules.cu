@@ -604,6 +604,7 @@ extern "C" sv_status sv_logits_process(const void *logits, void *out, sv_dtype d
     if (rules->bias_begin && (rules->n_bias < 0 ||
                               (rules->n_bias > 0 && (!rules->bias_tokens || !rules->bias_values))))
         return SV_ERR_ARG;
+    if (rules->bias_begin && rules->n_bias > (1 << 30)) return SV_ERR_SHAPE;   // entry + thread stays an int
     if (rules->mask) {
         if (rules->n_masks < 1) return SV_ERR_ARG;
         if (!rules->mask_index && static_cast<long long>(B) * P > rules->n_masks) return SV_ERR_SHAPE;

@@ -83,6 +83,7 @@ def _rules(**kw):
     (dict(history=_history(output_counts=None)), ARG),
     (dict(bias_begin=A[0], n_bias=3), ARG), (dict(bias_begin=A[0], n_bias=-1), ARG),
     (dict(mask=A[0], n_masks=0), ARG), (dict(mask=A[0], n_masks=19), SHAPE),
+    (dict(bias_begin=A[0], bias_tokens=A[1], bias_values=A[2], n_bias=2**30 + 1), SHAPE),
 ])
 def test_process_rules(kw, code):
     assert _process(_rules(**kw)) == code
