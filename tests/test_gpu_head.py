@@ -100,8 +100,20 @@ def test_head_few_tokens_of_a_large_vocabulary(V):
         h.check(h.x(M, 1), "float32")
 
 
+# Blocks of 128 k of a warp's share: 1, 2, 3, 5, 9 and unequal ones, four (the
+# large vocabulary) or sixteen warps to a tile, several tiles a warp.
+@pytest.mark.parametrize("V,H", [(40000, 512), (40000, 640), (40000, 1536), (40000, 2112), (40000, 2560), (40000, 4608),
+                                 (6000, 2048), (6000, 4160), (6000, 6144), (6000, 10240)])
+@pytest.mark.parametrize("group,zero,scale", [(128, False, "bfloat16"), (64, True, "float32"), (32, True, "bfloat16")])
+def test_head_few_tokens_whatever_a_warps_share(V, H, group, zero, scale):
+    h = Head(H // group * group, V, group, zero, scale, seed=V + H)
+    for M in (2, 10):
+        h.check(h.x(M, 1), "float32")
+
+
 @pytest.mark.parametrize("M", [17, 40, 64, 100, 200])
-@pytest.mark.parametrize("H,group,zero", [(384, 128, False), (128, 128, True), (96, 32, True), (448, 64, False)])
+@pytest.mark.parametrize("H,group,zero", [(384, 128, False), (128, 128, True), (96, 32, True), (448, 64, False),
+                                          (1120, 32, True), (2112, 64, True), (1408, 128, False)])
 def test_head_several_tiles_a_block(M, H, group, zero):
     # three tiles of 128 rows for some blocks; odd and even numbers of groups
     h = Head(H, 2 * 148 * 128 + 130, group, zero, "bfloat16", seed=M + H)
