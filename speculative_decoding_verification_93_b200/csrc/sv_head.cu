@@ -31,8 +31,8 @@
 //
 // Measured, V x H = 129280 x 4096, bf16 out, groups of 128 / 64 / 32 (the last
 // two with zero points):
-//      1 token   59 /  85 / 135 us (273 MB for groups of 128: 4.6 TB/s)
-//      9 tokens  77 / 112 / 154
+//      1 token   58 /  84 / 135 us (273 MB for groups of 128: 4.7 TB/s)
+//      9 tokens  80 / 110 / 154
 //     32 tokens  88 / 120 / 175
 //     64 tokens 102 / 133 / 209
 //    128 tokens 152 / 201 / 276
@@ -947,11 +947,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(HeadArgs a, int spl
         codes = a.codes + v * row_bytes + lo * 64 + t * (GROUP / 8);
         par = v * a.G + lo * kSubs;
     };
-    auto starts_set = [&](int block) { return (block - lo) * kSubs % 4 == 0; };
-    // The set that has been fetched becomes the one at hand.  That is left to
-    // its first block, except where the next set would be fetched before: the
-    // last set of a warp's share can have a single block.
-    bool taken = false;
+    // The set that was fetched becomes the one at hand.
     auto take_set = [&](int set, int from) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -959,20 +955,20 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(HeadArgs a, int spl
             if (ZERO) zp[set][r] = zero_pair(zp[from][r] & 15u);
         }
     };
-    // Asks for block f_kb of tile f_tile; `next` is the block before it.
-    auto fetch = [&](int u, int next) {
+    // That is left to the set's first block, whose loads have had the longest,
+    // but for a share whose last set has a single block: its set is taken
+    // before the next tile's first set is fetched over it.
+    bool lone = false;
+    auto fetch = [&](int u) {
+        if (lone && f_kb == lo) take_set(0, 1);
         if (f_tile >= tiles) return;
-        if (GROUP != 32 && starts_set(f_kb) && starts_set(next)) {
-            take_set(0, 1);
-            taken = true;
-        }
 #pragma unroll
         for (int q = 0; q < kSubs; ++q) {
             if (kSubs == 1 || f_kb * kSubs + q < a.G)
 #pragma unroll
             for (int r = 0; r < 4; ++r) ld_codes<kWords>(w[u][r] + q * kWords, codes + r * 8 * row_bytes + q * (GROUP / 2));
         }
-        if (starts_set(f_kb)) {
+        if ((f_kb - lo) * kSubs % 4 == 0) {
             const int set = GROUP == 32 ? u : 1;
             const int in = min(t, a.G - 1 - f_kb * kSubs);    // past the end: any
 #pragma unroll
@@ -1032,8 +1028,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(HeadArgs a, int spl
         return;
     }
     aim();
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) fetch(u, u == 0 ? lo + 1 : lo);   // (nothing before the first)
+    fetch(0);
+    lone = GROUP != 32 && (hi - 1 - lo) * kSubs % 4 == 0;
+    static_assert(kAhead == 2, "a set at hand and one on its way");
+    fetch(1);
     const uint32_t eight = zero_pair(8);
     int tile = first, kb = lo;
     while (tile < tiles) {
@@ -1041,8 +1039,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(HeadArgs a, int spl
         for (int u = 0; u < kAhead; ++u) {
             const int in_set = (kb - lo) * kSubs % 4;     // this block's first group in its set
             const int set = GROUP == 32 ? u : 0;
-            if (in_set == 0 && !taken) take_set(set, GROUP == 32 ? u : 1);
-            taken = false;
+            if (in_set == 0 && !(lone && kb + 1 == hi)) take_set(set, GROUP == 32 ? u : 1);
             const int xo = kb * 256;
 #pragma unroll
             for (int q = 0; q < kSubs; ++q) {
@@ -1089,7 +1086,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(HeadArgs a, int spl
 #pragma unroll
                         for (int i = 0; i < 4; ++i) acc[m][n][i] = fmaf(f[2 * m + i / 2], part[m][n][i], acc[m][n][i]);
             }
-            fetch(u, kb + 1 == hi ? lo : kb + 1);
+            fetch(u);
             if (++kb == hi) {
                 finish(tile);
                 kb = lo;
