@@ -708,7 +708,8 @@ typedef struct {
  *   lengths        device int32 [B], nullable (every position).
  *   workspace      device scratch of sv_head_w4_workspace_bytes(weight, B, P)
  *                  bytes, 16-byte aligned: the scheduled tokens of x in the
- *                  matrix unit's layout.  Calls that share a workspace must
+ *                  matrix unit's layout and, for a small vocabulary, the sums
+ *                  of the shares of a row's k.  Calls that share a workspace must
  *                  be stream-ordered.  NULL where that is 0 bytes: up to 16
  *                  tokens (B * P), unless V < 32 or B * P * H is too large
  *                  for x to be held on chip, take one launch without it.

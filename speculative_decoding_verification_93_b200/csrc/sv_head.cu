@@ -26,6 +26,8 @@
 //               write the logits: up to 128 tokens by turns (every second
 //               group each, the sums added at the end), above that one for
 //               each half of the tokens.
+// A vocabulary of few tiles has every tile's k shared out over several CTAs, whose
+// sums join_kernel adds in their order.
 // A in tensor memory keeps the widened weights (four times the bytes of the
 // codes) out of shared memory, whose bandwidth the B operand needs.
 //
@@ -92,6 +94,8 @@ struct HeadArgs {
     int *count;          // workspace: scheduled tokens
     int *rows;           // workspace [B * P]: output row of each packed token
     char *image;         // workspace: x images
+    int splits;          // of a row's k, each a CTA's; above 1 their sums are joined by join_kernel
+    float *part;         // workspace [splits, B * P, tiles, 128]: sums of each
     int32_t *status;
 };
 
@@ -357,6 +361,24 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
     return true;
 }
 
+// A CTA's share of a row's k: stages k0 .. k0 + nkb - 1, groups g0 .. g0 + G - 1.
+// Shares are whole chunks of kParGroups groups.
+struct Span {
+    int split, k0, nkb, g0, G;
+};
+
+__host__ __device__ __forceinline__ Span span_of(int split, int splits, int G, int nkb, int subs) {
+    const int chunks = (G + kParGroups - 1) / kParGroups, per = kParGroups / subs;   // stages of a chunk
+    const int c0 = chunks * split / splits, c1 = chunks * (split + 1) / splits;
+    Span p;
+    p.split = split;
+    p.g0 = c0 * kParGroups;
+    p.G = (c1 * kParGroups < G ? c1 * kParGroups : G) - p.g0;
+    p.k0 = c0 * per;
+    p.nkb = (c1 * per < nkb ? c1 * per : nkb) - p.k0;
+    return p;
+}
+
 __device__ __forceinline__ int warp_value(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // Eight codes to four pairs (code - zero) / 64 in bf16, exact.  A code in the
@@ -387,27 +409,28 @@ __device__ __forceinline__ float ld_scale(const HeadArgs &a, long long at) {
 // Codes of every stage (one lane).  start() asks for the first tile's before
 // the token count is known.
 template <typename Cfg> struct CodeCopy {
-    const HeadArgs &a;
+    const Span &span;
     const CUtensorMap *map;
     HeadBars &bar;
     char *ring;
-    int s = 0;
-    __device__ CodeCopy(const HeadArgs &a_, const CUtensorMap *m, HeadBars &b, char *r) : a(a_), map(m), bar(b), ring(r) {}
+    int tile0, s = 0;
+    __device__ CodeCopy(const Span &p, const CUtensorMap *m, HeadBars &b, char *r, int tile)
+        : span(p), map(m), bar(b), ring(r), tile0(tile) {}
     __device__ __forceinline__ void copy(int tile, int kb) {
         const int slot = s % Cfg::CS;
         mbar_arrive_expect_tx(&bar.cfull[slot], Cfg::kCodeBytes);
-        tma_tile(ring + slot * Cfg::kCodeBytes, map, kb * (Cfg::AK / 2), tile * kTileV, &bar.cfull[slot]);
+        tma_tile(ring + slot * Cfg::kCodeBytes, map, (span.k0 + kb) * (Cfg::AK / 2), tile * kTileV, &bar.cfull[slot]);
         ++s;
     }
     __device__ void start() {
-        for (int kb = 0; kb < min(a.nkb, Cfg::CS); ++kb) copy(blockIdx.x, kb);
+        for (int kb = 0; kb < min(span.nkb, Cfg::CS); ++kb) copy(tile0, kb);
     }
     __device__ bool run(const TokenPlan &t, int jobs) {
         bool ok = true;
         int q = 0;
         for (int job = 0; ok && job < jobs; ++job) {
-            const int tile = blockIdx.x + job / t.passes * gridDim.x;
-            for (int kb = 0; kb < a.nkb; ++kb, ++q) {
+            const int tile = tile0 + job / t.passes * gridDim.x;
+            for (int kb = 0; kb < span.nkb; ++kb, ++q) {
                 if (q < s) continue;      // asked for by start()
                 if (!mbar_wait(&bar.cempty[s % Cfg::CS], ((s / Cfg::CS) & 1) ^ 1, kHeadWaitNs)) { ok = false; break; }
                 copy(tile, kb);
@@ -422,13 +445,13 @@ template <typename Cfg> struct CodeCopy {
 
 // The x images of every stage (one lane).
 template <typename Cfg>
-__device__ bool x_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars &bar, char *xring) {
+__device__ bool x_role(const HeadArgs &a, const Span &span, const TokenPlan &t, int jobs, HeadBars &bar, char *xring) {
     const uint32_t bytes = t.per * Cfg::AK * 2;
     bool ok = true;
     int s = 0;
     for (int job = 0; ok && job < jobs; ++job) {
-        const char *src = a.image + static_cast<long long>(job % t.passes) * a.nkb * bytes;
-        for (int kb = 0; kb < a.nkb; ++kb, ++s) {
+        const char *src = a.image + (static_cast<long long>(job % t.passes) * a.nkb + span.k0) * bytes;
+        for (int kb = 0; kb < span.nkb; ++kb, ++s) {
             const int slot = s % Cfg::XS, old = s - Cfg::XS;
             if (old >= 0 && !mbar_wait(&bar.done[old % kDone], (old / kDone) & 1, kHeadWaitNs)) { ok = false; break; }
             mbar_arrive_expect_tx(&bar.xfull[slot], bytes);
@@ -443,15 +466,16 @@ __device__ bool x_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars
 // The matrix unit's instructions (warp 1, all lanes together).  Every
 // stage has all its batches; one past the last group has no products.
 template <typename Cfg, int GROUP>
-__device__ bool mma_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars &bar, const char *xring,
+__device__ bool mma_role(const HeadArgs &a, const Span &span, const TokenPlan &t, int jobs, HeadBars &bar, const char *xring,
                          uint32_t tmem) {
     const uint32_t nh = warp_value(t.nh), nh8 = nh * 8;
     constexpr int NH = Cfg::kNh;
-    const int stages = warp_value(jobs) * a.nkb, last_subs = (a.H - (a.nkb - 1) * Cfg::AK) / GROUP;
+    const int nkb = warp_value(span.nkb), stages = warp_value(jobs) * nkb;
+    const int last_subs = warp_value(span.G) - (nkb - 1) * Cfg::kSubs;   // groups of the last stage
     const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((nh >> 3) << 17) | ((kTileV >> 4) << 24);
     const uint32_t x0 = smem_desc(smem_u32(xring));
     constexpr int kUnit = GROUP < 64 ? GROUP : 64;
-    int left = a.nkb;                     // stages of the job still to come
+    int left = nkb;                       // stages of the job still to come
     uint32_t i = 0;                       // batch of a half
     bool ok = true;
 #pragma unroll 1
@@ -489,7 +513,7 @@ __device__ bool mma_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBa
         }
         if (!ok) break;
         mma_commit(&bar.done[s % kDone]);
-        if (--left == 0) left = a.nkb;
+        if (--left == 0) left = nkb;
     }
     // Nothing of the matrix unit is in flight when tensor memory is freed: the
     // last stage's commit covers all before it.  After a wait that ran out,
@@ -503,20 +527,21 @@ __device__ bool mma_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBa
 // in shared memory, eight groups at a time, so that the rows' strided reads
 // are 16 and 8 bytes wide where the alignment allows it, made once for both
 // halves, and ahead of their use.
-__device__ bool param_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars &bar, ParChunk *ring) {
+__device__ bool param_role(const HeadArgs &a, const Span &span, const TokenPlan &t, int jobs, int tile0, HeadBars &bar,
+                           ParChunk *ring) {
     constexpr int kRows = kTileV / 32;
     const int lane = threadIdx.x & 31;
     const bool wide = !a.scale_f32 && a.G % 8 == 0 && (reinterpret_cast<uintptr_t>(a.scale) & 15) == 0 &&
                       (reinterpret_cast<uintptr_t>(a.zero) & 7) == 0;
     int c = 0;
     for (int job = 0; job < jobs; ++job) {
-        const int tile = blockIdx.x + job / t.passes * gridDim.x;
-        for (int g0 = 0; g0 < a.G; g0 += kParGroups, ++c) {
+        const int tile = tile0 + job / t.passes * gridDim.x;
+        for (int g0 = 0; g0 < span.G; g0 += kParGroups, ++c) {
             ParChunk &p = ring[c % kParSlots];
             long long at[kRows];
 #pragma unroll
             for (int r = 0; r < kRows; ++r)
-                at[r] = static_cast<long long>(min(tile * kTileV + r * 32 + lane, a.V - 1)) * a.G + g0;
+                at[r] = static_cast<long long>(min(tile * kTileV + r * 32 + lane, a.V - 1)) * a.G + span.g0 + g0;
             if (wide) {
                 uint4 u[kRows];
                 uint2 z[kRows];
@@ -542,7 +567,7 @@ __device__ bool param_role(const HeadArgs &a, const TokenPlan &t, int jobs, Head
                 for (int r = 0; r < kRows; ++r) {
 #pragma unroll
                     for (int q = 0; q < kParGroups; ++q) {
-                        const long long e = at[r] + min(q, a.G - 1 - g0);
+                        const long long e = at[r] + min(q, span.G - 1 - g0);
                         p.scale[q][r * 32 + lane] =
                             64.f * ld_scale(a, e);
                         if (a.zero) p.off[q][r * 32 + lane] = zero_pair(__ldg(a.zero + e) & 15u);
@@ -560,11 +585,11 @@ __device__ bool param_role(const HeadArgs &a, const TokenPlan &t, int jobs, Head
 // this one's are widened.  Four pieces to a round of the loop (17 tokens of
 // 129280 x 4096, group 128: 89 us; two 93, one 99).
 template <typename Cfg, int GROUP>
-__device__ bool widen_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars &bar, const char *ring,
+__device__ bool widen_role(const HeadArgs &a, const Span &span, int jobs, HeadBars &bar, const char *ring,
                            const ParChunk *par, uint32_t tmem, int wi) {
     constexpr int kRowBytes = Cfg::AK / 2, kPieces = Cfg::AK / 32, kEach = GROUP / 32;   // pieces of a stage, a group
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
-    const int stages = jobs * a.nkb, chunks = (a.G + kParGroups - 1) / kParGroups;
+    const int stages = jobs * span.nkb, chunks = (span.G + kParGroups - 1) / kParGroups;
     const int r = quarter * 32 + lane;
     // The copy's swizzle: 16-byte pieces of 128-byte (64-byte) rows.
     const int swz = kRowBytes == 128 ? r & 7 : (r >> 1) & 3;
@@ -583,7 +608,7 @@ __device__ bool widen_role(const HeadArgs &a, const TokenPlan &t, int jobs, Head
     };
     // Zero point of piece q of the stage at kb.
     auto zero_of = [&](int q) {
-        const int gi = min(kb * Cfg::kSubs + q / kEach, a.G - 1), c = c0 + gi / kParGroups;
+        const int gi = min(kb * Cfg::kSubs + q / kEach, span.G - 1), c = c0 + gi / kParGroups;
         while (have < c)
             if (!next_chunk(true)) return false;
         off = par[c % kParSlots].off[gi % kParGroups][r];
@@ -595,7 +620,7 @@ __device__ bool widen_role(const HeadArgs &a, const TokenPlan &t, int jobs, Head
         if (!warp_wait(&bar.cfull[s % Cfg::CS], (s / Cfg::CS) & 1)) return false;
         row = ring + s % Cfg::CS * Cfg::kCodeBytes + r * kRowBytes;
         u = *reinterpret_cast<const uint4 *>(row + swz * 16);
-        while (kb >= a.nkb) { kb -= a.nkb; c0 += chunks; }
+        while (kb >= span.nkb) { kb -= span.nkb; c0 += chunks; }
         return !a.zero || zero_of(0);
     };
     if (wi < stages && !first(wi)) return false;
@@ -687,19 +712,29 @@ __device__ __forceinline__ void write_logits(T *out, int V, const float (&y)[N],
     }
 }
 
+// The same for a share's sums, `next` apart from token to token.
+template <int N>
+__device__ __forceinline__ void write_share(float *to, long long next, const float (&y)[N], int first, int step, int live) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int at = first + n / 4 * step + n % 4;
+        if (at < live) to[at * next] = y[n];
+    }
+}
+
 // A thread owns one vocabulary row: of half h, or with one half of every second
 // group (h, h + 2, ...).
 template <typename Cfg>
-__device__ bool accumulate_role(const HeadArgs &a, const TokenPlan &t, int jobs, HeadBars &bar,
+__device__ bool accumulate_role(const HeadArgs &a, const Span &span, const TokenPlan &t, int jobs, int tile0, HeadBars &bar,
                                 const ParChunk *par, float *sums, uint32_t tmem, int h) {
     constexpr int NH = Cfg::kNh, kRows = (NH + 31) / 32;
     constexpr bool kWhole = Cfg::kHalves == 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarter = warp & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const int batches = a.nkb * Cfg::kSubs;   // of a job and half; one past the last group has no products
+    const int batches = span.nkb * Cfg::kSubs;   // of a job and half; one past the last group has no products
     int i = 0, slot = 0, phase = 0;       // batch; slot and phase of the parameter ring
     for (int job = 0; job < jobs; ++job) {
-        const int tile = blockIdx.x + job / t.passes * gridDim.x, pass = job % t.passes;
+        const int tile = tile0 + job / t.passes * gridDim.x, pass = job % t.passes;
         const int v = tile * kTileV + quarter * 32 + lane;
         // Output rows of these tokens, 32 to a register across the lanes.
         const int t0 = pass * t.per + (kWhole ? 0 : h * t.nh), live = min(t.nh, t.count - t0);
@@ -712,7 +747,7 @@ __device__ bool accumulate_role(const HeadArgs &a, const TokenPlan &t, int jobs,
         for (int n = 0; n < NH; ++n) acc[n] = 0.f;
         constexpr int kStep = kWhole ? 2 : 1;
 #pragma unroll 1
-        for (int g0 = 0; g0 < a.G; g0 += kParGroups) {
+        for (int g0 = 0; g0 < span.G; g0 += kParGroups) {
             // This chunk's scales of the row; those past the last group are not used.
             if (!warp_wait(&bar.pfull[slot], phase)) return false;
             const float *scale = &par[slot].scale[kWhole ? h : 0][quarter * 32 + lane];
@@ -723,7 +758,7 @@ __device__ bool accumulate_role(const HeadArgs &a, const TokenPlan &t, int jobs,
                 const float sc = *scale;
                 if (!warp_wait(&bar.dfull[db], (at / Cfg::DB) & 1)) return false;
                 tc_fence_after();
-                if (g0 + j < a.G) add_batch<Cfg>(acc, lanes + db * NH, sc, t.nh);
+                if (g0 + j < span.G) add_batch<Cfg>(acc, lanes + db * NH, sc, t.nh);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.dempty[db]);
@@ -734,6 +769,11 @@ __device__ bool accumulate_role(const HeadArgs &a, const TokenPlan &t, int jobs,
         }
         const bool inside = v < a.V;
         const long long vo = v;
+        // A share's sums: token t0 + n of this tile.
+        float *share = nullptr;
+        if (a.splits > 1)
+            share = a.part + ((static_cast<long long>(span.split) * a.B * a.P + t0) * a.tiles + tile) * kTileV + quarter * 32 + lane;
+        const long long next = static_cast<long long>(a.tiles) * kTileV;
         if constexpr (kWhole) {
             // Each warpgroup takes every second four tokens of both.  (No
             // branches: code that runs once a job is fetched as it runs, and
@@ -754,10 +794,12 @@ __device__ bool accumulate_role(const HeadArgs &a, const TokenPlan &t, int jobs,
             for (int n = 0; n < NH / 2; ++n) mine[n] += buf[h * Cfg::kSums + n * kTileV];
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.summed);
-            if (a.out_f32) write_logits(static_cast<float *>(a.out) + vo, a.V, mine, rows, 4 * h, 8, live, inside);
+            if (share) write_share(share, next, mine, 4 * h, 8, live);
+            else if (a.out_f32) write_logits(static_cast<float *>(a.out) + vo, a.V, mine, rows, 4 * h, 8, live, inside);
             else write_logits(static_cast<__nv_bfloat16 *>(a.out) + vo, a.V, mine, rows, 4 * h, 8, live, inside);
         } else {
-            if (a.out_f32) write_logits(static_cast<float *>(a.out) + vo, a.V, acc, rows, 0, 4, live, inside);
+            if (share) write_share(share, next, acc, 0, 4, live);
+            else if (a.out_f32) write_logits(static_cast<float *>(a.out) + vo, a.V, acc, rows, 0, 4, live, inside);
             else write_logits(static_cast<__nv_bfloat16 *>(a.out) + vo, a.V, acc, rows, 0, 4, live, inside);
         }
     }
@@ -775,7 +817,11 @@ head_kernel(HeadArgs a, const __grid_constant__ CUtensorMap map) {
     ParChunk *par = reinterpret_cast<ParChunk *>(cring + Cfg::CS * Cfg::kCodeBytes);
     float *sums = reinterpret_cast<float *>(par + kParSlots);
     const int tid = threadIdx.x, warp = warp_value(tid >> 5), lane = tid & 31, wg = warp >> 2;
-    CodeCopy<Cfg> codes(a, &map, bar, cring);
+    // Whole rows, tile by tile, or (few tiles) one share of one tile.
+    const int split = a.splits > 1 ? static_cast<int>(blockIdx.x) / a.tiles : 0;
+    const int tile0 = static_cast<int>(blockIdx.x) - split * a.tiles;
+    const Span span = span_of(split, a.splits, a.G, a.nkb, Cfg::kSubs);
+    CodeCopy<Cfg> codes(span, &map, bar, cring, tile0);
     if (tid == 0) {
         for (int i = 0; i < Cfg::CS; ++i) { mbar_init(&bar.cfull[i], 1); mbar_init(&bar.cempty[i], 4); }
         for (int i = 0; i < Cfg::XS; ++i) mbar_init(&bar.xfull[i], 1);
@@ -802,8 +848,7 @@ head_kernel(HeadArgs a, const __grid_constant__ CUtensorMap map) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = warp_value(bar.tmem);
-    const int my_tiles = (a.tiles - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) /
-                         static_cast<int>(gridDim.x);
+    const int my_tiles = (a.tiles - tile0 + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
     const int jobs = my_tiles * t.passes;
     bool ok = true;
     if (wg == 0) {
@@ -811,18 +856,18 @@ head_kernel(HeadArgs a, const __grid_constant__ CUtensorMap map) {
         if (warp == 0) {
             if (lane == 0) ok = codes.run(t, jobs);
         } else if (warp == 1) {
-            ok = mma_role<Cfg, GROUP>(a, t, jobs, bar, xring, tmem);
+            ok = mma_role<Cfg, GROUP>(a, span, t, jobs, bar, xring, tmem);
         } else if (warp == 2) {
-            if (lane == 0) ok = x_role<Cfg>(a, t, jobs, bar, xring);
+            if (lane == 0) ok = x_role<Cfg>(a, span, t, jobs, bar, xring);
         } else {
-            ok = param_role(a, t, jobs, bar, par);
+            ok = param_role(a, span, t, jobs, tile0, bar, par);
         }
     } else if (wg <= Cfg::WW) {
         regs_less<Cfg::kRegsW>();
-        ok = widen_role<Cfg, GROUP>(a, t, jobs, bar, cring, par, tmem, wg - 1);
+        ok = widen_role<Cfg, GROUP>(a, span, jobs, bar, cring, par, tmem, wg - 1);
     } else {
         regs_more<Cfg::kRegsA>();
-        ok = accumulate_role<Cfg>(a, t, jobs, bar, par, sums, tmem, wg - 1 - Cfg::WW);
+        ok = accumulate_role<Cfg>(a, span, t, jobs, tile0, bar, par, sums, tmem, wg - 1 - Cfg::WW);
     }
     if (!ok && a.status) atomicOr(a.status, SV_NOTE_TIMEOUT);
     __syncwarp();
@@ -830,6 +875,30 @@ head_kernel(HeadArgs a, const __grid_constant__ CUtensorMap map) {
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_free(tmem, kTmemCols);
+}
+
+// The shares' sums of each logit, in their order.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(HeadArgs a) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int slot = blockIdx.x, v = (blockIdx.y * kJoinThreads + threadIdx.x) * 4, width = a.tiles * kTileV;
+    if (slot >= __ldcg(a.count) || v >= a.V) return;
+    const long long next = static_cast<long long>(a.B) * a.P * width;
+    const float *from = a.part + static_cast<long long>(slot) * width + v;
+    float4 y = *reinterpret_cast<const float4 *>(from);
+    for (int i = 1; i < a.splits; ++i) {
+        const float4 z = *reinterpret_cast<const float4 *>(from + i * next);
+        y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
+    }
+    const float w[4] = {y.x, y.y, y.z, y.w};
+    const long long o = static_cast<long long>(__ldcg(a.rows + slot)) * a.V + v;
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+        if (v + n < a.V) {
+            if (a.out_f32) store_logit(static_cast<float *>(a.out) + o + n, w[n]);
+            else store_logit(static_cast<__nv_bfloat16 *>(a.out) + o + n, w[n]);
+        }
 }
 
 // ---------------------------------------------------------------------------
@@ -1149,8 +1218,31 @@ static bool few(const sv_w4 *w, int M) {
     return M <= kFewTokens && w->V >= kFewRows && few_smem(M, w->H) <= kFewSmem;
 }
 
+// Shares of a row's k: as many as the SMs of a B200 allow beside the tiles.  The
+// longest share must be kSplitSaves stages shorter than the row, or the third
+// launch costs more than it saves (20 tokens: 1152 x 1952, groups of 128, one
+// stage less 10.7 to 13.1 us; 960 x 2830, groups of 64, two less 12.1 to 12.4 at
+// 52 tokens; 1600 x 3000, groups of 32, five less 18.1 to 13.4; 4608 x 2752 19 to
+// 13; 336 tokens of 12288 x 1000 185 to 42).  Up to kSplitTokens tokens the
+// shares' sums (76 KB a token at most) stay in L2.
+constexpr int kSms = 148, kSplitSaves = 3, kSplitTokens = 1024;
+
+static int splits_for(const sv_w4 *w, int M) {
+    const int ak = ak_for(nh_for(M)), nkb = (w->H + ak - 1) / ak, G = w->H / w->group, subs = ak / w->group;
+    const int tiles = (w->V + kTileV - 1) / kTileV, chunks = (G + kParGroups - 1) / kParGroups;
+    const int n = kSms / tiles < chunks ? kSms / tiles : chunks;
+    if (n < 2 || M > kSplitTokens) return 1;
+    int longest = 0;
+    for (int i = 0; i < n; ++i) {
+        const int k = span_of(i, n, G, nkb, subs).nkb;
+        if (k > longest) longest = k;
+    }
+    return nkb - longest >= kSplitSaves ? n : 1;
+}
+
 struct HeadPlan {
-    size_t off_rows, off_image, bytes;
+    size_t off_rows, off_image, off_part, bytes;
+    int splits;
 };
 
 static HeadPlan head_plan(const sv_w4 *w, int B, int P) {
@@ -1162,7 +1254,10 @@ static HeadPlan head_plan(const sv_w4 *w, int B, int P) {
     // Whatever the scheduled count is, it packs into at most as many passes
     // as M does, each of at most that many tokens.
     const size_t most = halves_for(M) * nh, passes = (M + most - 1) / most;
-    p.bytes = p.off_image + passes * most * nkb * ak * 2ull;
+    p.off_part = align(p.off_image + passes * most * nkb * ak * 2ull);
+    p.splits = splits_for(w, M);
+    const size_t tiles = (w->V + kTileV - 1) / kTileV;
+    p.bytes = p.off_part + (p.splits > 1 ? p.splits * M * tiles * kTileV * sizeof(float) : 0);
     return p;
 }
 
@@ -1205,7 +1300,7 @@ static cudaError_t launch_head(const HeadArgs &a, const CUtensorMap &map, cudaSt
         if (e == cudaSuccess) attr_set[dev & 63].store(true, std::memory_order_release);
     }
     if (e != cudaSuccess) return e;
-    return launch_pdl(head_kernel<HALVES, NH, GROUP>, dim3(a.tiles < sms ? a.tiles : sms), dim3(Cfg::kThreads), Cfg::kSmem,
+    return launch_pdl(head_kernel<HALVES, NH, GROUP>, dim3(a.splits > 1 ? a.splits * a.tiles : a.tiles < sms ? a.tiles : sms), dim3(Cfg::kThreads), Cfg::kSmem,
                       st, a, map);
 }
 
@@ -1259,6 +1354,8 @@ extern "C" sv_status sv_head_w4(const sv_w4 *weight, const void *x, int B, int P
     a.count = reinterpret_cast<int *>(w);
     a.rows = reinterpret_cast<int *>(w + p.off_rows);
     a.image = w + p.off_image;
+    a.splits = p.splits;
+    a.part = reinterpret_cast<float *>(w + p.off_part);
     a.status = status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int packs = M < sv::kPackGrid ? M : sv::kPackGrid;
@@ -1275,5 +1372,8 @@ extern "C" sv_status sv_head_w4(const sv_w4 *weight, const void *x, int B, int P
     case 128: e = sv::launch_group<1, 128>(a, map, st); break;
     default: e = sv::launch_group<2, 96>(a, map, st); break;
     }
+    if (e == cudaSuccess && a.splits > 1)
+        e = sv::launch_pdl(sv::join_kernel, dim3(M, (a.V + 4 * sv::kJoinThreads - 1) / (4 * sv::kJoinThreads)),
+                           dim3(sv::kJoinThreads), 0, st, a);
     return sv::note_cuda(e);
 }

@@ -100,6 +100,21 @@ def test_head_few_tokens_of_a_large_vocabulary(V):
         h.check(h.x(M, 1), "float32")
 
 
+@pytest.mark.parametrize("M", [20, 50, 100, 200, 1030])
+@pytest.mark.parametrize("H,V,group,zero", [(4608, 1000, 128, False), (2112, 701, 64, True), (1600, 515, 32, True),
+                                            (12288, 129, 128, True), (4096, 9000, 64, False), (2048, 1, 32, False)])
+def test_head_long_rows_of_a_small_vocabulary(M, H, V, group, zero):
+    # few tiles: several blocks share each tile's k
+    h = Head(H, V, group, zero, "float32" if zero else "bfloat16", seed=M + H)
+    P = 5 if M % 5 == 0 else 1
+    x = h.x(M // P, P)
+    lengths = torch.from_numpy(h.rng.integers(-1, P + 1, M // P).astype(np.int32)).cuda()
+    for out in ("float32", "bfloat16"):
+        h.check(x, out)
+        h.check(x, out, lengths, 1)
+    assert torch.equal(h.run(x, "float32"), h.run(x, "float32"))
+
+
 # Blocks of 128 k of a warp's share: 1, 2, 3, 5, 9 and unequal ones, four (the
 # large vocabulary) or sixteen warps to a tile, several tiles a warp.
 @pytest.mark.parametrize("V,H", [(40000, 512), (40000, 640), (40000, 1536), (40000, 2112), (40000, 2560), (40000, 4608),
