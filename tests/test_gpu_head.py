@@ -200,6 +200,30 @@ def test_head_on_streams_and_in_a_graph():
                 plain.check(outs[i].double().cpu().numpy(), *want[i])
 
 
+@pytest.mark.parametrize("M", [1, 20, 140])
+def test_head_of_a_small_vocabulary_replayed(M):
+    # a graph whose input changes between replays, beside eager calls on another stream
+    h = Head(4608, 1000, 128, True, "bfloat16", seed=M)
+    xs = [h.x(M, 1) for _ in range(3)]
+    want = [h.want(x, "float32") for x in xs]
+    x, outs = xs[0].clone(), [torch.zeros(M, 1, 1000, device="cuda") for _ in range(2)]
+    need = sv.sv_head_w4_workspace_bytes(h.weight, M, 1)
+    ws = [torch.empty(max(need, 16), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        sv.sv_head_w4(h.weight, x, outs[0], ws[0])
+    for i in range(3):
+        x.copy_(xs[i])
+        torch.cuda.synchronize()
+        graph.replay()
+        sv.sv_head_w4(h.weight, xs[2], outs[1], ws[1], stream=side)
+        torch.cuda.synchronize()
+        plain.check(outs[0].double().cpu().numpy(), *want[i])
+        plain.check(outs[1].double().cpu().numpy(), *want[2])
+        for o in outs:
+            o.zero_()
+
+
 def test_head_from_two_host_threads():
     # threads that have made no CUDA call before, one stream each
     h = Head(512, 2000, 64, True, "bfloat16", seed=13)
