@@ -637,11 +637,11 @@ typedef struct {
  * seen(v) = c(v) > 0 or v in the prompt:
  *   z1 = z / repetition if seen and z > 0;  z * repetition if seen;  else z
  *   z2 = z1 - frequency * c - presence * [c > 0]
- *   z3 = z2 + bias(v)
+ *   z3 = z2 + bias(v);  -inf if bias(v) is -inf
  *   out = z3 where the mask allows v, -inf where it does not,
- * in fp32, rounded once to `dtype`.  A forbidden logit is -inf whatever the
- * logit was.  A bias of -inf bans its token; of a token listed twice the
- * later entry counts.
+ * in fp32, rounded once to `dtype`.  A logit that a mask forbids or a bias of
+ * -inf bans is -inf whatever it was, +inf and NaN too.  Of a token listed twice
+ * the later valid entry counts.
  *
  *   logits, out    device [B, P, Vs] of `dtype`; out may be logits (then
  *                  only the logits that change are touched) or must not

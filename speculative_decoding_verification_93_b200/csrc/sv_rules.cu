@@ -315,6 +315,9 @@ __device__ __forceinline__ void copy_position(const RuleArgs &a, int b, int p, i
 
 __device__ __forceinline__ bool valid_bias(float v) { return !isnan(v) && !(isinf(v) && v > 0.f); }
 
+// A ban gives -inf whatever the logit was: the sum of +inf or NaN with it is NaN.
+__device__ __forceinline__ float biased(float z, float v) { return v == kNegInf ? kNegInf : z + v; }
+
 // The token of bias entry e has another before e1, which counts in its place.
 __device__ __forceinline__ bool listed_again(const RuleArgs &a, int e, int e1) {
     const int t = __ldg(a.bias_tokens + e);
@@ -531,7 +534,7 @@ __global__ void __launch_bounds__(RuleCfg<IN_PLACE>::kThreads, RuleCfg<IN_PLACE>
                     const int p = u + k * units;
                     if (p >= np || !(word[k] >> (t & 31) & 1u) || replaced) continue;
                     float y = penalise(a, r, sm, lv, c, p, ndraft, widen<ESIZE>(z[k]));
-                    if (bias >= 0) y += sm.bvalue[bias];
+                    if (bias >= 0) y = biased(y, sm.bvalue[bias]);
                     st_logit<ESIZE>(a.out + at + p * vec, y);
                 }
                 q += dr;
@@ -566,7 +569,7 @@ __global__ void __launch_bounds__(RuleCfg<IN_PLACE>::kThreads, RuleCfg<IN_PLACE>
             if (!allowed(mask_row(a, sm.mask[p]), t)) continue;
             float z = widen<ESIZE>(raw);
             if (penal) z = penalise(a, r, sm, lv, c, p, ndraft, z);
-            st_logit<ESIZE>(a.out + to, z + v);
+            st_logit<ESIZE>(a.out + to, biased(z, v));
         }
     }
 

@@ -439,3 +439,24 @@ def test_rules_on_streams_and_in_a_graph():
         torch.cuda.synchronize()
         plain.check(out.cpu().double().numpy(), *want[0])
         plain.check(z[1].cpu().double().numpy(), *want[1])
+
+
+@pytest.mark.parametrize("n_more", [0, 300])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_a_bias_of_minus_infinity_bans_whatever_the_logit_was(dtype, n_more):
+    """n_more further biases in the chunk: none, and more than a CTA lists."""
+    V = 2000
+    c = Case(2, 3, V, dtype, seed=37, n_bias=0, masks=None)
+    c.bias = [{}, {}]
+    c.rep[:] = 1.0
+    c.freq[:] = c.pres[:] = 0.25
+    for i, v in enumerate([np.inf, np.nan, -np.inf, torch.finfo(DT[dtype]).min]):
+        c.z[..., i::9] = v
+    banned = np.arange(0, 40)
+    for b in range(2):
+        c.bias[b] = {int(t): -np.inf for t in banned}
+        c.bias[b].update({1000 + t: 0.5 for t in range(n_more)})
+    want, bound = c.want()
+    want[..., banned], bound[..., banned] = -np.inf, 0.0
+    for in_place in (True, False):
+        c.check(in_place, want=(want, bound))
