@@ -663,7 +663,10 @@ typedef struct {
  *                  invalid penalty keeps it neutral (SV_ROW_BAD_PENALTY),
  *                  an invalid slot reads an empty history, an invalid bias
  *                  entry is left out (SV_ROW_BAD_TOKEN, SV_ROW_BAD_BIAS), an
- *                  invalid mask index masks nothing.  A mask without an
+ *                  invalid mask index masks nothing.  A row's bias list
+ *                  is read whole for every 8192 tokens of its vocabulary (2048
+ *                  with a separate output): a rule for most of the vocabulary
+ *                  is better given as a mask.  A mask without an
  *                  allowed token leaves only -inf and raises
  *                  SV_ROW_EMPTY_MASK (detected only when `status` is given);
  *                  sv_verify would emit token 0 with SV_NOTE_CDF_FALLBACK

@@ -18,7 +18,9 @@
 //      that position's copy, while its lines are still in the caches.
 //      (Penalising inside the copy was slower, 66 against 59 us at
 //      64 x 5 x 129280 bf16: a few lanes of a warp had work.)
-//   D. the chunk's biased tokens, in place as further items of C.
+//   D. the chunk's biased tokens, in place as further items of C; where a chunk
+//      has more than a CTA lists, token by token.  Either way a token's last entry
+//      is found once, and a list costs its length in every CTA of its row.
 // In place, B and C/D touch disjoint elements (forbidden, allowed).
 //
 // Measured, bf16, 256 x 9 x 129280 in place, 1214 positions scheduled, 1.9 M
@@ -39,7 +41,7 @@
 
 namespace sv {
 
-constexpr int kBiasList = 256;
+constexpr int kBiasList = 256;           // biases of a chunk that a CTA lists
 
 // In place a CTA mostly waits (for its row's parameters, its planes, then a few
 // logits each), so it takes many tokens; a copy is bound by its bytes, and small
@@ -105,13 +107,17 @@ template <bool IN_PLACE> struct RuleSmem {
     uint32_t bias[Cfg::kPlane];
     uint32_t prompt[Cfg::kPlane];
     uint32_t output[Cfg::kPlane];
-    unsigned short list[Cfg::kChunk];   // touched tokens without a bias, ascending
+    alignas(4) unsigned short list[Cfg::kChunk];   // touched tokens without a bias, ascending
     int count[IN_PLACE ? 1 : Cfg::kChunk];   // output count of each listed token
+    // More than kBiasList biases: the last entry of each of kLast tokens, where
+    // the list (the counts) stood.
+    static constexpr int kLast = IN_PLACE ? Cfg::kChunk / 2 : Cfg::kChunk;
+    __device__ __forceinline__ int *last() { return IN_PLACE ? reinterpret_cast<int *>(list) : count; }
     int wsum[Cfg::kThreads / 32];
     int nbias;                       // valid biases of this chunk, and the first of them:
     int blist[kBiasList];            //   entry
     unsigned short btoken[kBiasList];   //   local token
-    float bvalue[kBiasList];
+    float bvalue[kBiasList];         //   value; NaN where a later entry counts
     int dup;                         // a biased token of this chunk is listed twice
     int dtok[SV_MAX_K];              // local token of each draft, -1 if not in the chunk
     int mask[SV_MAX_K + 1];          // mask of each position, -1 for none
@@ -318,12 +324,13 @@ __device__ __forceinline__ bool valid_bias(float v) { return !isnan(v) && !(isin
 // A ban gives -inf whatever the logit was: the sum of +inf or NaN with it is NaN.
 __device__ __forceinline__ float biased(float z, float v) { return v == kNegInf ? kNegInf : z + v; }
 
-// The token of bias entry e has another before e1, which counts in its place.
-__device__ __forceinline__ bool listed_again(const RuleArgs &a, int e, int e1) {
-    const int t = __ldg(a.bias_tokens + e);
-    for (int f = e + 1; f < e1; ++f)
-        if (__ldg(a.bias_tokens + f) == t && valid_bias(__ldg(a.bias_values + f))) return true;
-    return false;
+// Of a token listed twice the later entry counts: the others' values become NaN.
+template <bool IN_PLACE> __device__ __forceinline__ void drop_replaced(RuleSmem<IN_PLACE> &sm) {
+    for (int i = threadIdx.x; i < sm.nbias; i += RuleCfg<IN_PLACE>::kThreads) {
+        bool replaced = false;
+        for (int j = 0; j < sm.nbias; ++j) replaced |= sm.btoken[j] == sm.btoken[i] && sm.blist[j] > sm.blist[i];
+        if (replaced) sm.bvalue[i] = __builtin_nanf("");
+    }
 }
 
 // Status: the row's parameters, and masks of its first np positions that allow
@@ -446,6 +453,7 @@ __global__ void __launch_bounds__(RuleCfg<IN_PLACE>::kThreads, RuleCfg<IN_PLACE>
         sm.output[tid] = wo;
     }
     __syncthreads();
+    if (sm.dup && sm.nbias <= kBiasList) drop_replaced(sm);
     // The touched tokens in ascending order: places by a scan over the words.
     uint32_t touched = tid < Cfg::kPlane ? (wp | wo | sm.draft[tid]) & ~sm.bias[tid] : 0u;
     int incl = __popc(touched);
@@ -528,13 +536,13 @@ __global__ void __launch_bounds__(RuleCfg<IN_PLACE>::kThreads, RuleCfg<IN_PLACE>
                     }
                 }
                 const int c = output_count(a, r, sm, c0, lv);
-                const bool replaced = bias >= 0 && sm.dup && listed_again(a, sm.blist[bias], e1);
+                const float more = bias >= 0 ? sm.bvalue[bias] : 0.f;
 #pragma unroll
                 for (int k = 0; k < kPositions; ++k) {
                     const int p = u + k * units;
-                    if (p >= np || !(word[k] >> (t & 31) & 1u) || replaced) continue;
+                    if (p >= np || !(word[k] >> (t & 31) & 1u) || isnan(more)) continue;
                     float y = penalise(a, r, sm, lv, c, p, ndraft, widen<ESIZE>(z[k]));
-                    if (bias >= 0) y = biased(y, sm.bvalue[bias]);
+                    if (bias >= 0) y = biased(y, more);
                     st_logit<ESIZE>(a.out + at + p * vec, y);
                 }
                 q += dr;
@@ -543,33 +551,41 @@ __global__ void __launch_bounds__(RuleCfg<IN_PLACE>::kThreads, RuleCfg<IN_PLACE>
             }
         }
     }
-    // D. Biased tokens: the last entry of a token counts.
-    if (sm.nbias > (IN_PLACE ? kBiasList : 0)) {
-        const bool listed = sm.nbias <= kBiasList;
-        const long long pairs = static_cast<long long>(listed ? sm.nbias : e1 - e0) * np;
-        for (long long q = tid; q < pairs; q += kThreads) {
-            const int i = static_cast<int>(q / np), p = static_cast<int>(q - static_cast<long long>(i) * np);
-            int e = e0 + i, lv;
-            float v;
-            if (listed) {
-                e = sm.blist[i];
-                lv = sm.btoken[i];
-                v = sm.bvalue[i];
-            } else {
+    // D. Biased tokens.  Position p of token lv, with bias v.
+    auto bias_logit = [&](int lv, int p, int c, float v) {
+        const long long to = row_at + p * vec + lv * ESIZE;
+        const uint32_t raw = ld_raw<ESIZE>(a.in + to);
+        if (!allowed(mask_row(a, sm.mask[p]), a.v0 + c0 + lv)) return;
+        float z = widen<ESIZE>(raw);
+        if (penal) z = penalise(a, r, sm, lv, c, p, ndraft, z);
+        st_logit<ESIZE>(a.out + to, biased(z, v));
+    };
+    if (sm.nbias > kBiasList) {
+        for (int l0 = 0; l0 < n; l0 += sm.kLast) {
+            const int m = min(sm.kLast, n - l0);
+            __syncthreads();                  // what stood there has been read
+            for (int lv = tid; lv < m; lv += kThreads) sm.last()[lv] = -1;
+            __syncthreads();
+            for (int e = e0 + tid; e < e1; e += kThreads) {
                 const int t = __ldg(a.bias_tokens + e);
-                lv = t - a.v0 - c0;
-                v = __ldg(a.bias_values + e);
-                if (t < 0 || t >= a.V || lv < 0 || lv >= n || !valid_bias(v)) continue;
+                if (t < 0 || t >= a.V || !valid_bias(__ldg(a.bias_values + e))) continue;
+                const int lv = t - a.v0 - c0 - l0;
+                if (lv >= 0 && lv < m) atomicMax(&sm.last()[lv], e);
             }
-            const int t = a.v0 + c0 + lv;
-            if (sm.dup && listed_again(a, e, e1)) continue;
-            const long long to = row_at + p * vec + lv * ESIZE;
-            const uint32_t raw = ld_raw<ESIZE>(a.in + to);
-            const int c = penal ? output_count(a, r, sm, c0, lv) : 0;
-            if (!allowed(mask_row(a, sm.mask[p]), t)) continue;
-            float z = widen<ESIZE>(raw);
-            if (penal) z = penalise(a, r, sm, lv, c, p, ndraft, z);
-            st_logit<ESIZE>(a.out + to, biased(z, v));
+            __syncthreads();
+            for (int lv = tid; lv < m; lv += kThreads) {
+                const int e = sm.last()[lv];
+                if (e < 0) continue;
+                const float v = __ldg(a.bias_values + e);
+                const int c = penal ? output_count(a, r, sm, c0, l0 + lv) : 0;
+                for (int p = 0; p < np; ++p) bias_logit(l0 + lv, p, c, v);
+            }
+        }
+    } else if (!IN_PLACE) {
+        for (int q = tid; q < sm.nbias * np; q += kThreads) {
+            const int i = q / np, lv = sm.btoken[i];
+            const float v = sm.bvalue[i];
+            if (!isnan(v)) bias_logit(lv, q - i * np, penal ? output_count(a, r, sm, c0, lv) : 0, v);
         }
     }
 

@@ -460,3 +460,62 @@ def test_a_bias_of_minus_infinity_bans_whatever_the_logit_was(dtype, n_more):
     want[..., banned], bound[..., banned] = -np.inf, 0.0
     for in_place in (True, False):
         c.check(in_place, want=(want, bound))
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("n", [255, 256, 257, 700, 5000])
+def test_tokens_listed_again_in_long_lists(n, dtype):
+    """Lists around and past what a CTA keeps on chip, half of their tokens listed
+    again: the last valid entry counts, whatever chunk it lies in."""
+    V, B = 20011, 2
+    c = Case(B, 3, V, dtype, seed=41 + n, n_bias=0)
+    tokens, values, c.bias = [], [], []
+    for b in range(B):
+        few = c.rng.integers(0, 8192 if b else V, n // 2)   # row 1: all in one chunk in place
+        t = np.concatenate([few, c.rng.choice(few, n - n // 2)]).astype(np.int32)
+        v = c.rng.normal(0, 3, n).astype(np.float32)
+        v[c.rng.random(n) < 0.2] = -np.inf
+        v[c.rng.random(n) < 0.2] = np.nan
+        v[c.rng.random(n) < 0.1] = np.inf
+        c.bias.append({int(x): float(y) for x, y in zip(t, v) if y < np.inf})   # NaN: false
+        tokens.append(t)
+        values.append(v)
+    base = c.rules()
+    r = sv.LogitRules(base.history, repetition=dev(c.rep), frequency=dev(c.freq),
+                      presence=dev(c.pres), bias_begin=dev(np.array([0, n, 2 * n], np.int32)),
+                      bias_tokens=dev(np.concatenate(tokens)),
+                      bias_values=dev(np.concatenate(values)),
+                      mask=dev(plain.pack(c.mask)), mask_index=dev(c.index))
+    want = c.want()
+    for in_place in (True, False):
+        c.check(in_place, rules=r, status=sv.SV_ROW_BAD_BIAS, want=want)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("near,far", [(8192, 0), (200, 60000)])
+def test_one_repeated_bias_does_not_cost_more_than_its_entry(near, far, in_place):
+    """The same list with and without one repeated token.  Each entry is read
+    once or twice either way, so the times are alike (a factor of three is
+    left for noise); a scan of the list for each entry would make them differ
+    by the list's length."""
+    V, P = 129280, 9
+    z = torch.zeros(1, P, V, device="cuda")
+    out = z if in_place else torch.zeros_like(z)
+    took = []
+    for repeat in (False, True):
+        tokens = np.concatenate([np.arange(near), 20000 + np.arange(far)]).astype(np.int32)
+        if repeat:
+            tokens[1] = tokens[0]
+        rules = sv.LogitRules(bias_begin=dev(np.array([0, near + far], np.int32)),
+                              bias_tokens=dev(tokens),
+                              bias_values=torch.full((near + far,), 1.0, device="cuda"))
+        times = []
+        for _ in range(6):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            sv.sv_logits_process(z, out, rules)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        took.append(min(times))
+    assert took[1] <= 3 * took[0] + 0.05, f"{took[0]:.3f} ms without, {took[1]:.3f} ms with"
