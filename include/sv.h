@@ -17,6 +17,8 @@
  *    device memory, never frees caller memory and never synchronises the
  *    stream; all work is enqueued on `stream` (a cudaStream_t passed as
  *    void*, NULL = legacy default stream) and completes asynchronously.
+ *  - Device pointers to int32, uint32 and float32 must be aligned to 4 bytes
+ *    (sv_history_*, sv_logits_process and sv_head_w4 refuse others).
  *  - Argument errors are detected on the host before anything is launched
  *    and returned synchronously; nothing is written in that case.
  *  - Data errors that can only be seen on the device never fault or trap:

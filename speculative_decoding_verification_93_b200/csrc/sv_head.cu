@@ -1331,6 +1331,7 @@ extern "C" sv_status sv_head_w4(const sv_w4 *weight, const void *x, int B, int P
         return SV_ERR_ARG;
     if (reinterpret_cast<uintptr_t>(weight->scale) & (weight->scale_dtype == SV_F32 ? 3 : 1)) return SV_ERR_ARG;
     if (reinterpret_cast<uintptr_t>(out) & (out_dtype == SV_F32 ? 3 : 1)) return SV_ERR_ARG;
+    if (sv::misaligned4(lengths, status)) return SV_ERR_ARG;
     const bool few = sv::few(weight, B * P);
     if (!few && !workspace) return SV_ERR_ARG;
     const sv::HeadPlan p = sv::head_plan(weight, B, P);

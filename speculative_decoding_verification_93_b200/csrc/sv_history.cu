@@ -98,9 +98,7 @@ __global__ void __launch_bounds__(256) history_reset_kernel(HistoryArgs a) {
 
 static sv_status history_check(const sv_history *h) {
     if (!h || !h->prompt_bits || !h->output_bits || !h->output_counts) return SV_ERR_ARG;
-    if ((reinterpret_cast<uintptr_t>(h->prompt_bits) | reinterpret_cast<uintptr_t>(h->output_bits) |
-         reinterpret_cast<uintptr_t>(h->output_counts)) & 3)
-        return SV_ERR_ARG;
+    if (misaligned4(h->prompt_bits, h->output_bits, h->output_counts)) return SV_ERR_ARG;
     if (h->R < 1 || h->V < 1 || h->V > SV_MAX_V) return SV_ERR_SHAPE;
     return SV_OK;
 }
@@ -131,7 +129,7 @@ extern "C" sv_status sv_history_add(const sv_history *history, const int32_t *sl
     if (kind != SV_HISTORY_PROMPT && kind != SV_HISTORY_OUTPUT) return SV_ERR_ARG;
     if (B < 0 || S < 0 || (!slots && B > history->R)) return SV_ERR_SHAPE;
     if (B == 0 || S == 0) return SV_OK;
-    if (!tokens) return SV_ERR_ARG;
+    if (!tokens || sv::misaligned4(slots, tokens, lens, status)) return SV_ERR_ARG;
     sv::HistoryArgs a = sv::history_args(history);
     a.slots = slots;
     a.tokens = tokens;
@@ -151,6 +149,7 @@ extern "C" sv_status sv_history_reset(const sv_history *history, const int32_t *
     if (const sv_status e = sv::history_check(history)) return e;
     if (n < 0 || (!slots && n > history->R)) return SV_ERR_SHAPE;
     if (n == 0) return SV_OK;
+    if (sv::misaligned4(slots, status)) return SV_ERR_ARG;
     sv::HistoryArgs a = sv::history_args(history);
     a.slots = slots;
     a.n = n;

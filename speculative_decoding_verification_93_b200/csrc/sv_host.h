@@ -1,6 +1,7 @@
 // sv_host.h -- host-side helpers shared by the library's translation units.
 #pragma once
 
+#include <cstdint>
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 
@@ -28,6 +29,11 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Some of these pointers to 4-byte elements is not aligned to them (null is).
+template <typename... P> bool misaligned4(const P *...p) {
+    return ((reinterpret_cast<uintptr_t>(p) | ...) & 3) != 0;
 }
 
 // NVTX range over one library call, named after the entry point, so that a

@@ -611,9 +611,15 @@ extern "C" sv_status sv_logits_process(const void *logits, void *out, sv_dtype d
     if ((in_at | out_at) & (es - 1)) return SV_ERR_ARG;
     const size_t bytes = static_cast<size_t>(B) * P * Vs * es;
     if (in_at != out_at && in_at < out_at + bytes && out_at < in_at + bytes) return SV_ERR_ARG;
+    if (sv::misaligned4(draft_tokens, lengths, status, rules->slots, rules->repetition, rules->frequency,
+                        rules->presence, rules->bias_begin, rules->bias_tokens, rules->bias_values, rules->mask,
+                        rules->mask_index))
+        return SV_ERR_ARG;
     sv::RuleArgs a = {};
     if (const sv_history *h = rules->history) {
-        if (!h->prompt_bits || !h->output_bits || !h->output_counts) return SV_ERR_ARG;
+        if (!h->prompt_bits || !h->output_bits || !h->output_counts ||
+            sv::misaligned4(h->prompt_bits, h->output_bits, h->output_counts))
+            return SV_ERR_ARG;
         if (h->R < 1 || h->V != V || (!rules->slots && B > h->R)) return SV_ERR_SHAPE;
         a.prompt = h->prompt_bits;
         a.output = h->output_bits;

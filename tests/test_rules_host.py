@@ -166,3 +166,32 @@ def test_binding_refuses():
 def test_plain_bit_planes_round_trip():
     flags = np.random.default_rng(0).random((3, 77)) < 0.4
     assert np.array_equal(plain.unpack(plain.pack(flags), 77), flags)
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_misaligned_arrays_refused(off):
+    """Every int32, uint32 and float32 array, before anything could be launched."""
+    L, bad = sv.lib(), A[2] + off
+    h = _history()
+    for kind in (0, 1):
+        for slots, tokens, lens, status in ((bad, A[1], None, None), (None, bad, None, None),
+                                            (None, A[1], bad, None), (None, A[1], None, bad)):
+            assert L.sv_history_add(h, slots, 2, tokens, 5, lens, 0, kind, status, None) == ARG
+    assert L.sv_history_reset(h, bad, 2, None, None) == ARG
+    assert L.sv_history_reset(h, None, 2, bad, None) == ARG
+    for name in ("prompt_bits", "output_bits", "output_counts"):
+        assert _process(_rules(history=_history(**{name: bad}))) == ARG, name
+    for name in ("slots", "repetition", "frequency", "presence", "bias_begin", "bias_tokens",
+                 "bias_values", "mask", "mask_index"):
+        kw = dict(bias_begin=A[0], bias_tokens=A[0], bias_values=A[0], n_bias=3, mask=A[0],
+                  n_masks=20, mask_index=A[0])
+        kw[name] = bad
+        assert _process(_rules(**kw)) == ARG, name
+    assert _process(drafts=bad) == ARG
+    assert _process(lengths=bad) == ARG
+    assert L.sv_logits_process(A[1], A[1], sv.SV_BF16, 4, 5, 1000, 0, 1000, None, 0, 0, None, 0,
+                               bd._Rules(), bad, None) == ARG
+    for B in (2, 20):
+        assert _head(B=B, lengths=bad) == ARG
+        w = bd._W4(A[0], A[4], None, sv.SV_BF16, 100, 256, 64)
+        assert L.sv_head_w4(w, A[1], B, 3, None, 0, A[2], sv.SV_BF16, A[3], 1 << 40, bad, None) == ARG
