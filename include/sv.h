@@ -714,8 +714,9 @@ typedef struct {
  *   workspace      device scratch of sv_head_w4_workspace_bytes(weight, B, P)
  *                  bytes, 16-byte aligned: the scheduled tokens of x in the
  *                  matrix unit's layout and, for a small vocabulary, the sums
- *                  of the shares of a row's k.  Calls that share a workspace must
- *                  be stream-ordered.  NULL where that is 0 bytes: up to 16
+ *                  of the shares of a row's k.  One made for a batch serves every
+ *                  smaller one of the same weights.  Calls that share a workspace
+ *                  must be stream-ordered.  NULL where that is 0 bytes: up to 16
  *                  tokens (B * P), unless V < 32 or B * P * H is too large
  *                  for x to be held on chip, take one launch without it.
  *   status         device int32, nullable; SV_NOTE_TIMEOUT is OR-ed in if an

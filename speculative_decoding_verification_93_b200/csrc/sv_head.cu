@@ -1314,7 +1314,11 @@ template <int HALVES, int NH> static cudaError_t launch_group(const HeadArgs &a,
 
 extern "C" size_t sv_head_w4_workspace_bytes(const sv_w4 *weight, int B, int P) {
     if (sv::head_check(weight, B, P) != SV_OK || B == 0 || sv::few(weight, B * P)) return 0;
-    return sv::head_plan(weight, B, P).bytes;
+    // Enough for every smaller batch too: up to kSplitTokens tokens there may be
+    // sums of shares, which larger batches do without.
+    const size_t own = sv::head_plan(weight, B, P).bytes;
+    const size_t split = B * P > sv::kSplitTokens ? sv::head_plan(weight, sv::kSplitTokens, 1).bytes : 0;
+    return own > split ? own : split;
 }
 
 extern "C" sv_status sv_head_w4(const sv_w4 *weight, const void *x, int B, int P,

@@ -365,3 +365,15 @@ def test_head_rules_verification_and_history_together(B, K, V, seed):
             plain_history.add(b, emitted)
         assert np.array_equal(history.output_counts.cpu().numpy(), plain_history.counts)
         assert np.array_equal(history.output_bits.cpu().numpy(), plain.pack(plain_history.counts > 0))
+
+
+def test_head_one_workspace_for_every_batch():
+    # 1000 rows: the shares of k have sums in the workspace up to 1024 tokens
+    h = Head(2048, 1000, 128, False, "bfloat16", seed=23)
+    most = 1100
+    ws = torch.empty(sv.sv_head_w4_workspace_bytes(h.weight, most, 1), dtype=torch.uint8, device="cuda")
+    for M in (most, 1024, 300, 40, 7):
+        x, out = h.x(M, 1), torch.zeros(M, 1, 1000, device="cuda")
+        sv.sv_head_w4(h.weight, x, out, ws)
+        torch.cuda.synchronize()
+        plain.check(out.double().cpu().numpy(), *h.want(x, "float32"))

@@ -195,3 +195,16 @@ def test_misaligned_arrays_refused(off):
         assert _head(B=B, lengths=bad) == ARG
         w = bd._W4(A[0], A[4], None, sv.SV_BF16, 100, 256, 64)
         assert L.sv_head_w4(w, A[1], B, 3, None, 0, A[2], sv.SV_BF16, A[3], 1 << 40, bad, None) == ARG
+
+
+@pytest.mark.parametrize("V,H,group", [(1000, 12288, 128), (1000, 4096, 32), (33, 4096, 64),
+                                       (31, 256, 32), (2752, 4608, 128), (10007, 1120, 32),
+                                       (129280, 4096, 128), (64, 32768, 64)])
+def test_head_workspace_serves_smaller_batches(V, H, group):
+    """A workspace made for the largest batch is large enough for every smaller one."""
+    w = bd._W4(A[0], A[4], None, sv.SV_BF16, V, H, group)
+    sizes = list(range(1, 1200)) + list(range(1200, 5000, 61)) + [1 << 14, 1 << 17, 1 << 20]
+    need = [sv.lib().sv_head_w4_workspace_bytes(w, M, 1) for M in sizes]
+    for i in range(1, len(need)):
+        assert need[i] >= need[i - 1], (sizes[i - 1:i + 1], need[i - 1:i + 1])
+    assert sv.lib().sv_head_w4_workspace_bytes(w, 1 << 10, 1 << 10) == need[-1]
