@@ -646,7 +646,7 @@ extern "C" sv_status sv_logits_process(const void *logits, void *out, sv_dtype d
     a.lengths = lengths; a.extra = extra;
     a.slots = rules->slots;
     a.rep = rules->repetition; a.freq = rules->frequency; a.pres = rules->presence;
-    a.bias_begin = rules->n_bias > 0 ? rules->bias_begin : nullptr;
+    a.bias_begin = rules->bias_begin;
     a.bias_tokens = rules->bias_tokens; a.bias_values = rules->bias_values;
     a.n_bias = rules->n_bias;
     a.mask = rules->mask; a.n_masks = rules->n_masks; a.mask_index = rules->mask_index;

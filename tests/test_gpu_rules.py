@@ -519,3 +519,16 @@ def test_one_repeated_bias_does_not_cost_more_than_its_entry(near, far, in_place
             times.append(a.elapsed_time(b))
         took.append(min(times))
     assert took[1] <= 3 * took[0] + 0.05, f"{took[0]:.3f} ms without, {took[1]:.3f} ms with"
+
+
+def test_a_bias_list_over_empty_arrays_is_reported():
+    c = Case(2, 2, 300, "float32", seed=43, n_bias=0, masks=None)
+    c.bias = [{}, {}]
+    base = c.rules()
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    for begin, bits in (([0, 0, 0], 0), ([0, 0, 5], sv.SV_ROW_BAD_BIAS)):
+        r = sv.LogitRules(base.history, repetition=dev(c.rep), frequency=dev(c.freq),
+                          presence=dev(c.pres), bias_begin=dev(np.array(begin, np.int32)),
+                          bias_tokens=none, bias_values=none.float())
+        for in_place in (True, False):
+            c.check(in_place, rules=r, status=bits)
