@@ -720,7 +720,8 @@ typedef struct {
  *                  tokens (B * P), unless V < 32 or B * P * H is too large
  *                  for x to be held on chip, take one launch without it.
  *   status         device int32, nullable; SV_NOTE_TIMEOUT is OR-ed in if an
- *                  internal wait ran out (out is then undefined).
+ *                  internal wait ran out (out is then undefined).  With NULL
+ *                  nothing tells: sv_head_w4 has returned SV_OK by then.
  * The same inputs give the same bits on every call.  Never synchronises.
  * Returns SV_OK, SV_ERR_ARG, SV_ERR_SHAPE, SV_ERR_DTYPE, SV_ERR_WORKSPACE or
  * SV_ERR_CUDA.  sv_head_w4_workspace_bytes also returns 0 for unsupported

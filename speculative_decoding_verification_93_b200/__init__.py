@@ -7,7 +7,7 @@ loaded, every call raises.
 """
 from ._binding import (  # noqa: F401
     SV_BF16, SV_F32, SV_HISTORY_OUTPUT, SV_HISTORY_PROMPT, SV_NOTE_CDF_FALLBACK,
-    SV_NOTE_ZERO_RESIDUAL, SV_ROW_BAD_BIAS, SV_ROW_BAD_LENGTH, SV_ROW_BAD_MASK,
+    SV_NOTE_TIMEOUT, SV_NOTE_ZERO_RESIDUAL, SV_ROW_BAD_BIAS, SV_ROW_BAD_LENGTH, SV_ROW_BAD_MASK,
     SV_ROW_BAD_PENALTY, SV_ROW_BAD_SLOT, SV_ROW_BAD_TEMPERATURE, SV_ROW_BAD_TOKEN,
     SV_ROW_EMPTY_MASK, SVError, LogitRules, TokenHistory, W4Weight,
     lib, library_path, sv_philox4x32_10,

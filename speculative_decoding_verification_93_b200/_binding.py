@@ -11,7 +11,7 @@ import torch
 
 SV_F32, SV_BF16 = 0, 1
 SV_ROW_BAD_TOKEN, SV_ROW_BAD_LENGTH, SV_ROW_BAD_TEMPERATURE = 1, 2, 4
-SV_NOTE_ZERO_RESIDUAL, SV_NOTE_CDF_FALLBACK = 8, 16
+SV_NOTE_ZERO_RESIDUAL, SV_NOTE_CDF_FALLBACK, SV_NOTE_TIMEOUT = 8, 16, 32
 SV_ROW_BAD_SLOT, SV_ROW_BAD_PENALTY, SV_ROW_BAD_BIAS = 64, 128, 256
 SV_ROW_BAD_MASK, SV_ROW_EMPTY_MASK = 512, 1024
 SV_HISTORY_PROMPT, SV_HISTORY_OUTPUT = 0, 1

@@ -377,3 +377,50 @@ def test_head_one_workspace_for_every_batch():
         sv.sv_head_w4(h.weight, x, out, ws)
         torch.cuda.synchronize()
         plain.check(out.double().cpu().numpy(), *h.want(x, "float32"))
+
+
+def test_chain_with_slots_and_one_status():
+    """The serving loop as documented: rows mapped to slots, one status word
+    through all four calls, a slot given back between the steps."""
+    B, K, V, R = 6, 3, 1500, 11
+    rng = np.random.default_rng(3)
+    h = Head(512, V, 64, True, "bfloat16", seed=3)
+    dev = lambda x: torch.as_tensor(np.ascontiguousarray(x)).cuda()  # noqa: E731
+    history, want = sv.TokenHistory.empty(R, V, "cuda"), plain.History(R, V)
+    slot = rng.permutation(R)[:B].astype(np.int32)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    prompt = rng.integers(0, V, (B, 20)).astype(np.int32)
+    sv.sv_history_add(history, dev(prompt), kind=sv.SV_HISTORY_PROMPT, slots=dev(slot), status=st)
+    for b in range(B):
+        want.add(slot[b], prompt[b], prompt=True)
+    pen = [rng.uniform(lo, hi, B).astype(np.float32) for lo, hi in ((1, 1.5), (0, 0.4), (0, 0.4))]
+    ws = torch.empty(max(16, sv.sv_head_w4_workspace_bytes(h.weight, B, K + 1)), dtype=torch.uint8,
+                     device="cuda")
+    for step in range(3):
+        lengths = rng.integers(0, K + 1, B).astype(np.int32)
+        drafts = rng.integers(0, V, (B, K)).astype(np.int32)
+        allowed = rng.random((2, V)) < 0.7
+        index = rng.integers(-1, 2, (B, K + 1)).astype(np.int32)
+        rules = sv.LogitRules(history, dev(slot), *map(dev, pen), mask=dev(plain.pack(allowed)),
+                              mask_index=dev(index))
+        x, ln, dr = h.x(B, K + 1), dev(lengths), dev(drafts)
+        zt, zd = torch.zeros(B, K + 1, V, device="cuda"), torch.randn(B, K, V, device="cuda")
+        sv.sv_head_w4(h.weight, x, zt, ws, lengths=ln, extra=1, status=st)
+        raw = zt.double().cpu().numpy()
+        sv.sv_logits_process(zt, zt, rules, dr, ln, extra=1, status=st)
+        tokens, accepted = sv.verify(zt, zd, dr, ln, torch.ones(B, device="cuda"), seed=step, status=st)
+        sv.sv_history_add(history, tokens, lens=accepted, extra=1, slots=dev(slot), status=st)
+        assert int(st) & ~(sv.SV_NOTE_CDF_FALLBACK | sv.SV_NOTE_ZERO_RESIDUAL) == 0
+        got, tok, acc = zt.double().cpu().numpy(), tokens.cpu().numpy(), accepted.cpu().numpy()
+        for b in range(B):
+            s, n = slot[b], int(lengths[b]) + 1
+            masks = [allowed[i] if i >= 0 else None for i in index[b]]
+            out, bound = plain.process(raw[b], "float32", drafts[b], 0, n, want.prompt[s], want.counts[s],
+                                       *(float(p[b]) for p in pen), {}, masks)
+            plain.check(got[b], out, bound)
+            want.add(s, tok[b, :acc[b] + 1])
+        sv.sv_history_reset(history, slots=dev(slot[step:step + 1]), status=st)
+        want.counts[slot[step]], want.prompt[slot[step]] = 0, False
+        assert np.array_equal(history.output_counts.cpu().numpy(), want.counts)
+        assert np.array_equal(history.output_bits.cpu().numpy(), plain.pack(want.counts > 0))
+        assert np.array_equal(history.prompt_bits.cpu().numpy(), plain.pack(want.prompt))

@@ -2,6 +2,8 @@
 bad arguments are refused before any CUDA call, by the library and by the
 Python binding."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -208,3 +210,11 @@ def test_head_workspace_serves_smaller_batches(V, H, group):
     for i in range(1, len(need)):
         assert need[i] >= need[i - 1], (sizes[i - 1:i + 1], need[i - 1:i + 1])
     assert sv.lib().sv_head_w4_workspace_bytes(w, 1 << 10, 1 << 10) == need[-1]
+
+
+def test_binding_names_every_status_bit():
+    header = open(os.path.join(os.path.dirname(__file__), "..", "include", "sv.h")).read()
+    bits = re.findall(r"#define (SV_(?:ROW|NOTE)_\w+)\s+(\d+)", header)
+    assert len(bits) == 11
+    for name, value in bits:
+        assert getattr(sv, name) == int(value), name
