@@ -424,3 +424,17 @@ def test_chain_with_slots_and_one_status():
         assert np.array_equal(history.output_counts.cpu().numpy(), want.counts)
         assert np.array_equal(history.output_bits.cpu().numpy(), plain.pack(want.counts > 0))
         assert np.array_equal(history.prompt_bits.cpu().numpy(), plain.pack(want.prompt))
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_heads_of_random_sizes(seed):
+    rng = np.random.default_rng(2000 + seed)
+    group = int(rng.choice([32, 64, 128]))
+    H = group * int(np.exp(rng.uniform(0, np.log(8192 // group))))
+    V = int(np.exp(rng.uniform(0, np.log(min(20000, 2e7 / H)))))
+    P = int(rng.choice([1, 2, 3, 5, 9]))
+    B = max(1, min(int(np.exp(rng.uniform(0, np.log(400)))), int(3e9 / (H * V)), 400) // P)
+    h = Head(H, V, group, bool(rng.random() < 0.5), str(rng.choice(["float32", "bfloat16"])), seed)
+    lengths = torch.from_numpy(rng.integers(-2, P + 3, B).astype(np.int32)).cuda() \
+        if rng.random() < 0.5 else None
+    h.check(h.x(B, P), str(rng.choice(["float32", "bfloat16"])), lengths, int(rng.integers(0, 2)))

@@ -532,3 +532,53 @@ def test_a_bias_list_over_empty_arrays_is_reported():
                           bias_tokens=none, bias_values=none.float())
         for in_place in (True, False):
             c.check(in_place, rules=r, status=bits)
+
+
+def test_history_of_more_entries_than_threads():
+    """The kernels start at most 148 * 64 * 256 = 2424832 threads."""
+    B, S, V = 300, 9001, 1000
+    tokens = torch.randint(0, V, (B, S), generator=torch.Generator().manual_seed(1), dtype=torch.int32)
+    h = sv.TokenHistory.empty(B, V, "cuda")
+    for kind in (sv.SV_HISTORY_PROMPT, sv.SV_HISTORY_OUTPUT):
+        sv.sv_history_add(h, tokens.cuda(), kind=kind)
+    counts = torch.zeros(B, V, dtype=torch.int32).scatter_add_(
+        1, tokens.long(), torch.ones_like(tokens)).numpy()
+    assert np.array_equal(h.output_counts.cpu().numpy(), counts)
+    for bits in (h.output_bits, h.prompt_bits):
+        assert np.array_equal(bits.cpu().numpy(), plain.pack(counts > 0))
+    R = 2500000                                  # slots of one word each
+    h = sv.TokenHistory.empty(R, 3, "cuda")
+    h.prompt_bits.fill_(5)
+    h.output_bits.fill_(6)
+    h.output_counts[:, 1:] = 7
+    sv.sv_history_reset(h, n=R - 1)
+    for t, last in ((h.prompt_bits, [5]), (h.output_bits, [6]), (h.output_counts, [0, 7, 7])):
+        assert not bool(t[:-1].any()) and t[-1].tolist() == last
+
+
+@pytest.mark.parametrize("v0,Vs", [(0, 10001), (5, 8192), (33, 9000), (8191, 1811), (10001, 1)])
+def test_rules_on_a_vocabulary_slice_in_fp32(v0, Vs):
+    c = Case(3, 3, 10002, "float32", seed=v0 + 1, v0=v0, Vs=Vs, slots=True)
+    want = c.want()
+    for in_place in (True, False):
+        c.check(in_place, want=want)
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_rules_of_random_batches(seed):
+    rng = np.random.default_rng(1000 + seed)
+    V = int(np.exp(rng.uniform(0, np.log(30000))))
+    P = int(rng.choice([1, 1, 2, 3, 5, 9, 17, 65]))
+    B = max(1, min(int(np.exp(rng.uniform(0, np.log(40)))), 300000 // (P * V)))
+    K = min(64, int(rng.choice([0, P - 1, P, P + 3])))
+    v0 = int(rng.choice([0, 0, rng.integers(0, V)]))
+    lengths = rng.integers(-2, P + 3, B).astype(np.int32) if rng.random() < 0.5 else None
+    c = Case(B, P, V, str(rng.choice(["float32", "bfloat16"])), seed=seed, K=K,
+             pos0=int(rng.choice([0, 0, rng.integers(0, 6)])), v0=v0,
+             Vs=int(rng.choice([V - v0, rng.integers(1, V - v0 + 1)])), lengths=lengths,
+             extra=int(rng.integers(0, 3)), n_bias=int(min(V, rng.choice([0, 1, 3, 16, 400]))),
+             masks=[None, "index", "all"][rng.integers(0, 3)], penalties=bool(rng.random() < 0.8),
+             slots=bool(rng.random() < 0.5), history=bool(rng.random() < 0.8))
+    want = c.want()
+    for in_place in (True, False):
+        c.check(in_place, want=want, shift=int(rng.integers(-9, 10)))
