@@ -675,7 +675,8 @@ typedef struct {
  *                  from such a position.
  *   status         device int32, nullable; bits OR-ed in.
  * Logit pointers must be aligned to their element size; vectors may start at
- * any alignment.  One launch, no workspace.
+ * any alignment (a separate output that lies otherwise to 16 bytes than the
+ * logits is copied element by element).  One launch, no workspace.
  * Returns SV_OK, SV_ERR_ARG, SV_ERR_SHAPE, SV_ERR_DTYPE or SV_ERR_CUDA.
  */
 sv_status sv_logits_process(const void *logits, void *out, sv_dtype dtype, int B, int P, int V,

@@ -3,7 +3,7 @@
 //
 // The product is computed transposed: D[v, token] = sum_k W[v, k] x[token, k]
 // with 128 vocabulary rows as the matrix unit's M and the tokens as its N,
-// so that few tokens waste little and every weight is read once.
+// so that few tokens waste little and every weight is read once for up to 192 tokens.
 //
 // Exactness.  code - zero is an integer of at most five bits, exact in bf16,
 // and so is its product with a bf16 x in fp32.  The scale is not folded into
@@ -32,13 +32,15 @@
 // codes) out of shared memory, whose bandwidth the B operand needs.
 //
 // Measured, V x H = 129280 x 4096, bf16 out, groups of 128 / 64 / 32 (the last
-// two with zero points):
-//      1 token   58 /  84 / 135 us (273 MB for groups of 128: 4.7 TB/s)
-//      9 tokens  80 / 110 / 154
-//     32 tokens  88 / 120 / 175
-//     64 tokens 102 / 133 / 209
-//    128 tokens 152 / 201 / 276
-//    192 tokens 192 / 231 / 389 (203 GFLOP: 1.06 PFLOP/s for groups of 128)
+// two with zero points), 600 calls over three heads in turn (on another board the
+// forms above 64 tokens took up to a tenth more, under its power cap):
+//      1 token   57 /  83 / 135 us (273 MB for groups of 128: 4.8 TB/s)
+//      9 tokens  80 / 111 / 154
+//     32 tokens  89 / 122 / 175
+//     64 tokens 103 / 134 / 206
+//    128 tokens 160 / 204 / 275
+//    192 tokens 208 / 247 / 381 (203 GFLOP: 0.98 PFLOP/s for groups of 128)
+//    200 tokens 335 / 420 / 676 (a second pass)
 // Every group costs a round of hand-overs (products, read-back, buffer free),
 // some 250 cycles whatever its length, and every 128 k a widening warpgroup
 // some 1000: neither memory nor the matrix unit (16 cycles a product at 32
@@ -904,9 +906,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(HeadArgs a) {
 // ---------------------------------------------------------------------------
 // 4. Few tokens: one launch, no tensor memory.
 //
-// With at most 16 tokens nothing but the weights' bytes costs, and the
-// hand-overs between roles above would set the pace (17 tokens of 129280 x
-// 4096 take 87 us there).  Here a warp does all of it for 32 vocabulary rows:
+// With at most 16 tokens the hand-overs between roles above would set the pace
+// (17 tokens of 129280 x 4096 take 89 us there).  Here a warp does all of it for
+// 32 vocabulary rows, and what it costs is to widen them (one token, groups of 128:
+// issue slots 59%, integer pipe 50%, DRAM 55%):
 // codes straight into registers, two blocks of 128 k ahead; widened there;
 // multiplied by mma.sync with the rows as M = 16 and the tokens as N = 8 or 16
 // (the matrix unit is idle most of the time, so its older path is enough);
@@ -1218,7 +1221,8 @@ static bool few(const sv_w4 *w, int M) {
     return M <= kFewTokens && w->V >= kFewRows && few_smem(M, w->H) <= kFewSmem;
 }
 
-// Shares of a row's k: as many as the SMs of a B200 allow beside the tiles.  The
+// Shares of a row's k: as many as the SMs of a B200 allow beside the tiles (not
+// those of the current device: the workspace's size must not depend on it).  The
 // longest share must be kSplitSaves stages shorter than the row, or the third
 // launch costs more than it saves (20 tokens: 1152 x 1952, groups of 128, one
 // stage less 10.7 to 13.1 us; 960 x 2830, groups of 64, two less 12.1 to 12.4 at

@@ -6,9 +6,12 @@
 // per token.  The planes are what a reader scans (V / 8 bytes instead of 4 V
 // bytes of counts); a count is looked up only where its bit is set.
 //
-// Both kernels are bound by their launch: 64 prompts of up to 4096 tokens take
-// 6.3 us cold under a profiler, and a call takes 5 us back to back, what issuing
-// it from Python costs, whatever its size.
+// At serving sizes history_add is bound by its launch: 64 prompts of up to 4096
+// tokens take 6.6 us cold under a profiler, and calls from Python take 5 us back to
+// back, what issuing them costs.  A reset reads V / 8 bytes of output bits a slot,
+// writes twice that, and zeroes the counts of the tokens that were emitted, each in
+// a sector of its own.  With L2 flushed, V = 129280: 4 slots 6 us, 256 slots 11
+// (after 800 emitted tokens each; 17 after 4000), 2048 slots 55.
 #include <climits>
 #include <cstdint>
 

@@ -24,13 +24,14 @@
 // In place, B and C/D touch disjoint elements (forbidden, allowed).
 //
 // Measured, bf16, 256 x 9 x 129280 in place, 1214 positions scheduled, 1.9 M
-// touched logits, a quarter of the rows masked: 74 us, of which penalties alone
-// take 39, masks alone 30 and a call without rules 9.  Touched logits lie alone
+// touched logits, a quarter of the rows masked: 80 us on fresh logits, 74 on the
+// same ones again, of which penalties alone take 39, masks alone 30 and a call
+// without rules 9.  Slots and a status word add less than 2.  Touched logits lie alone
 // in their sectors, so the DRAM moves 178 MB for the 66 MB that the rules name;
 // it is a third busy, the issue slots half: the rest is waiting for a few
 // logits at a time, CTA by CTA, six resident or five alike.
 // 64 x 5 x 129280 with a separate output: 54 us, 36 of them the copy (165 MB,
-// 4.6 TB/s); 128 x 17 x 129280 fp32, half of it scheduled: 242 us, 195 of them
+// 4.6 TB/s); 128 x 17 x 129280 fp32, half of it scheduled: 240 us, 195 of them
 // the copy (1.2 GB, 6.1 TB/s).
 #include <climits>
 #include <cstdint>
@@ -45,8 +46,8 @@ constexpr int kBiasList = 256;           // biases of a chunk that a CTA lists
 
 // In place a CTA mostly waits (for its row's parameters, its planes, then a few
 // logits each), so it takes many tokens; a copy is bound by its bytes, and small
-// CTAs keep more of them on their way.  At the size above
-// in place: 8192 tokens and 256 threads 74 us; chunks of 4096 tokens 91, 128
+// CTAs keep more of them on their way.  At the size above, in place on the same
+// logits again: 8192 tokens and 256 threads 74 us; chunks of 4096 tokens 91, 128
 // threads a CTA 93, 512 threads 112, chunks that grow with the token id 79.
 template <bool IN_PLACE> struct RuleCfg {
     static constexpr int kThreads = IN_PLACE ? 256 : 128;
