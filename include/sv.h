@@ -697,7 +697,8 @@ sv_status sv_logits_process(const void *logits, void *out, sv_dtype dtype, int B
 typedef struct {
     const uint8_t *codes;    /* device [V, H / 2]: code k in the low (even k) or high (odd k)
                                 half of byte k / 2; 16-byte aligned */
-    const void *scale;       /* device [V, H / group] of scale_dtype */
+    const void *scale;       /* device [V, H / group] of scale_dtype; below 2^122 (64 times a
+                                scale has to be finite) */
     const uint8_t *zero;     /* device [V, H / group], nullable (8): the low four bits count */
     sv_dtype scale_dtype;    /* SV_F32 or SV_BF16 */
     int V, H, group;         /* 1 <= V <= SV_MAX_V; group 32, 64 or 128; H a multiple of

@@ -438,3 +438,113 @@ def test_heads_of_random_sizes(seed):
     lengths = torch.from_numpy(rng.integers(-2, P + 3, B).astype(np.int32)).cuda() \
         if rng.random() < 0.5 else None
     h.check(h.x(B, P), str(rng.choice(["float32", "bfloat16"])), lengths, int(rng.integers(0, 2)))
+
+
+def test_head_of_more_than_four_gigabytes_of_codes():
+    V, H, group = 1 << 20, 8192, 32
+    g = torch.Generator(device="cuda").manual_seed(1)
+    codes = torch.randint(0, 256, (V, H // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scale = torch.rand(V, H // group, generator=g, device="cuda").bfloat16()
+    zero = torch.randint(0, 16, (V, H // group), generator=g, device="cuda", dtype=torch.uint8)
+    weight = sv.W4Weight(codes, scale, zero)
+    # the first rows, those around 2 GB of codes, the last
+    rows = torch.cat([torch.arange(a - 150, a + 150) for a in (150, V // 2, V - 150)]).cuda()
+    sub = codes[rows].cpu().numpy()
+    q = np.stack((sub & 15, sub >> 4), -1).reshape(len(rows), H)
+    for M in (2, 20):
+        x = torch.randn(M, 1, H, generator=g, device="cuda").bfloat16()
+        out = torch.zeros(M, 1, V, device="cuda")
+        need = sv.sv_head_w4_workspace_bytes(weight, M, 1)
+        sv.sv_head_w4(weight, x, out, torch.empty(max(need, 16), dtype=torch.uint8, device="cuda"))
+        want, bound = plain.head(x[:, 0].double().cpu().numpy(), q, scale[rows].double().cpu().numpy(),
+                                 zero[rows].double().cpu().numpy(), group, "float32")
+        plain.check(out[:, 0, rows].double().cpu().numpy(), want, bound)
+
+
+def test_head_of_more_than_four_gigabytes_of_logits():
+    V, M = 1 << 20, 2100
+    h = Head(32, V, 32, False, "float32", seed=29)
+    x = torch.randint(-3, 4, (M, 1, 32), dtype=torch.int8, device="cuda").bfloat16()
+    out = torch.full((M, 1, V), 55.0, device="cuda")
+    lengths = torch.ones(M, dtype=torch.int32, device="cuda")
+    lengths[M - 2] = 0
+    ws = torch.empty(sv.sv_head_w4_workspace_bytes(h.weight, M, 1), dtype=torch.uint8, device="cuda")
+    sv.sv_head_w4(h.weight, x, out, ws, lengths=lengths)
+    w = torch.from_numpy(h.codes.astype(np.float64) - 8).cuda() * h.scale.double().cuda()
+    for m in (0, 1023, 1024, 2047, 2048, M - 1):
+        want = (x[m].double() @ w.T)
+        # integers of at most 32 * 3 * 8 are exact; the scale's product rounds once
+        assert bool(((out[m].double() - want).abs() <= want.abs() * 2.0 ** -24).all())
+    assert bool((out[M - 2] == 55).all())
+
+
+@pytest.mark.parametrize("M", [3, 20, 140])
+def test_head_of_weights_written_just_before(M):
+    """Weights, scales and tokens that the stream writes right before each call."""
+    heads = [Head(1024, 5000, 64, True, "bfloat16", seed=s) for s in (31, 32)]
+    x = [h.x(M, 1) for h in heads]
+    want = [h.want(t, "float32") for h, t in zip(heads, x)]
+    w = [heads[0].weight.codes.clone(), heads[0].weight.scale.clone(), heads[0].weight.zero.clone()]
+    weight, xs = sv.W4Weight(*w), x[0].clone()
+    need = sv.sv_head_w4_workspace_bytes(weight, M, 1)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    outs = [torch.zeros(M, 1, 5000, device="cuda") for _ in range(6)]
+
+    def write(i):
+        for t, s in zip(w + [xs], (heads[i].weight.codes, heads[i].weight.scale, heads[i].weight.zero, x[i])):
+            torch.add(s, 0, out=t) if t.dtype != torch.uint8 else torch.bitwise_or(s, 0, out=t)
+    write(0)
+    torch.cuda.synchronize()
+    for n, out in enumerate(outs):
+        write(n % 2)
+        sv.sv_head_w4(weight, xs, out, ws)
+    torch.cuda.synchronize()
+    for n, out in enumerate(outs):
+        plain.check(out.double().cpu().numpy(), *want[n % 2])
+
+
+def test_chain_in_a_graph():
+    """Head, rules, verification and history captured once and replayed: each
+    replay goes on from the history that the one before left, as eager calls do."""
+    B, K, V = 12, 4, 3001
+    h = Head(512, V, 64, True, "bfloat16", seed=37)
+    rng = np.random.default_rng(37)
+    dev = lambda x: torch.as_tensor(np.ascontiguousarray(x)).cuda()  # noqa: E731
+    slot, pen = dev(rng.permutation(B + 3)[:B].astype(np.int32)), [
+        dev(rng.uniform(lo, hi, B).astype(np.float32)) for lo, hi in ((1, 1.5), (0, 0.4), (0, 0.4))]
+    mask, index = dev(plain.pack(rng.random((3, V)) < 0.6)), dev(rng.integers(-1, 3, (B, K + 1)).astype(np.int32))
+    x, ln = h.x(B, K + 1), dev(rng.integers(0, K + 1, B).astype(np.int32))
+    dr, zd = dev(rng.integers(0, V, (B, K)).astype(np.int32)), torch.randn(B, K, V, device="cuda")
+    temp = torch.ones(B, device="cuda")
+
+    def side():
+        """One copy of everything that a step writes, and the step."""
+        history = sv.TokenHistory.empty(B + 3, V, "cuda")
+        rules = sv.LogitRules(history, slot, *pen, mask=mask, mask_index=index)
+        zt = torch.zeros(B, K + 1, V, device="cuda")
+        tok = torch.zeros(B, K + 1, dtype=torch.int32, device="cuda")
+        acc = torch.zeros(B, dtype=torch.int32, device="cuda")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        ws = torch.empty(max(16, sv.sv_head_w4_workspace_bytes(h.weight, B, K + 1)), dtype=torch.uint8, device="cuda")
+        vws = torch.empty(sv.sv_verify_workspace_bytes(B, K, V, sv.SV_F32), dtype=torch.uint8, device="cuda")
+
+        def step():
+            sv.sv_head_w4(h.weight, x, zt, ws, lengths=ln, extra=1, status=st)
+            sv.sv_logits_process(zt, zt, rules, dr, ln, extra=1, status=st)
+            sv.sv_verify(zt, zd, dr, ln, temp, 5, tok, acc, vws, status=st)
+            sv.sv_history_add(history, tok, lens=acc, extra=1, slots=slot, status=st)
+        written = (zt, tok, acc, st, history.prompt_bits, history.output_bits, history.output_counts)
+        return step, written
+    eager, a = side()
+    captured, b = side()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured()
+    for _ in range(4):
+        eager()
+        graph.replay()
+        torch.cuda.synchronize()
+        for s, t in zip(a, b):
+            assert torch.equal(s, t)
+        assert int(a[3]) & ~(sv.SV_NOTE_CDF_FALLBACK | sv.SV_NOTE_ZERO_RESIDUAL) == 0
+    assert int(a[6].sum()) >= 4 * B

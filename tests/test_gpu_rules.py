@@ -582,3 +582,52 @@ def test_rules_of_random_batches(seed):
     want = c.want()
     for in_place in (True, False):
         c.check(in_place, want=want, shift=int(rng.integers(-9, 10)))
+
+
+def test_history_behind_four_gigabytes():
+    """Slots whose counts lie more than 2^32 elements behind the first one's."""
+    R, V = 34000, 129280                          # 4.4e9 counts
+    h = sv.TokenHistory.empty(R, V, "cuda")
+    slots = np.array([0, 16612, 33222, R - 1], np.int32)
+    rng = np.random.default_rng(3)
+    tokens = rng.integers(0, V, (4, 50)).astype(np.int32)
+    for kind in (sv.SV_HISTORY_PROMPT, sv.SV_HISTORY_OUTPUT):
+        sv.sv_history_add(h, dev(tokens), kind=kind, slots=dev(slots))
+    counts = np.zeros((4, V), np.int32)
+    for b in range(4):
+        np.add.at(counts[b], tokens[b], 1)
+    at = dev(slots).long()
+    assert np.array_equal(h.output_counts[at].cpu().numpy(), counts)
+    assert np.array_equal(h.prompt_bits[at].cpu().numpy(), plain.pack(counts > 0))
+    for in_place in (True, False):
+        z = torch.full((4, 1, V), 2.0, device="cuda")
+        out = z if in_place else torch.zeros_like(z)
+        sv.sv_logits_process(z, out, sv.LogitRules(h, dev(slots), frequency=torch.full((4,), 0.5, device="cuda")))
+        assert np.array_equal(out[:, 0].cpu().numpy(), 2.0 - 0.5 * counts.astype(np.float32))
+    assert int(h.output_counts.sum(1, dtype=torch.int32).sum()) == 200
+    sv.sv_history_reset(h, dev(slots[1:]))
+    assert int(h.output_counts.sum(1, dtype=torch.int32).sum()) == 50
+    assert np.array_equal(h.output_counts[0].cpu().numpy(), counts[0])
+    assert not bool(h.prompt_bits[at[1:]].any() or h.output_bits[at[1:]].any())
+
+
+def test_history_in_a_graph():
+    V, B = 500, 3
+    h, want = sv.TokenHistory.empty(B, V, "cuda"), plain.History(B, V)
+    rng = np.random.default_rng(4)
+    tokens = torch.zeros(B, 6, dtype=torch.int32, device="cuda")
+    one = dev(np.array([1], np.int32))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sv.sv_history_reset(h, one)
+        sv.sv_history_add(h, tokens)
+        sv.sv_history_add(h, tokens, kind=sv.SV_HISTORY_PROMPT)
+    for _ in range(3):
+        t = rng.integers(0, V, (B, 6)).astype(np.int32)
+        tokens.copy_(dev(t))
+        graph.replay()
+        want.counts[1], want.prompt[1] = 0, False
+        for b in range(B):
+            want.add(b, t[b])
+            want.add(b, t[b], prompt=True)
+        check_history(h, want)
